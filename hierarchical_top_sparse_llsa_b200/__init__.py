@@ -31,6 +31,8 @@ FLAG_FWD_TCGEN05 = 1
 FLAG_BWD_TCGEN05 = 2
 FLAG_FWD_MMA_SYNC = 4
 NOALLOC_SCRATCH_BYTES = 16 << 20
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN = 0, 1, 2, 3
 
 EXPORTED = (
     "llsa_pool",
@@ -46,6 +48,13 @@ EXPORTED = (
     "llsa_attn_bwd",
     "llsa_attn_bwd_noalloc",
     "llsa_reorder",
+    "llsa_rope_table",
+    "llsa_rope",
+    "llsa_rope_pool",
+    "llsa_cross_fwd_workspace_bytes",
+    "llsa_cross_bwd_workspace_bytes",
+    "llsa_cross_attn_fwd",
+    "llsa_cross_attn_bwd",
     "llsa_selftest_wait_timeout",
     "llsa_status_string",
     "llsa_version",
@@ -75,6 +84,21 @@ class LlsaIndices(ctypes.Structure):
 
 class LlsaCsr(ctypes.Structure):
     _fields_ = [("row_ptr", _PtrArr), ("col", _PtrArr)]
+
+
+class LlsaRopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("axes", ctypes.c_int), ("scaling", ctypes.c_int),
+        ("orig_len", ctypes.c_int), ("mscale", ctypes.c_float), ("base", ctypes.c_double),
+        ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+    ]
+
+
+class LlsaCrossDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int), ("N", ctypes.c_int), ("S", ctypes.c_int),
+        ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("flags", ctypes.c_int), ("sm_scale", ctypes.c_float),
+    ]
 
 
 # llsa_version() of the library whose struct layouts (llsa_desc above) this
@@ -122,6 +146,17 @@ def lib() -> ctypes.CDLL:
                                                      P(LlsaIndices), P(LlsaCsr), vp, vp, vp, vp, vp]),
             "llsa_reorder": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                             ctypes.c_int, vp, vp, ctypes.c_int, vp]),
+            "llsa_rope_table": (ctypes.c_int, [P(LlsaRopeDesc), ctypes.c_int, vp, vp, vp]),
+            "llsa_rope": (ctypes.c_int, [P(LlsaRopeDesc), ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, vp, ctypes.c_int, vp]),
+            "llsa_rope_pool": (ctypes.c_int, [P(LlsaDesc), P(LlsaRopeDesc), vp, ctypes.c_int, vp, vp, vp, vp, vp,
+                                              P(LlsaPyramid), vp]),
+            "llsa_cross_fwd_workspace_bytes": (ctypes.c_size_t, [P(LlsaCrossDesc)]),
+            "llsa_cross_bwd_workspace_bytes": (ctypes.c_size_t, [P(LlsaCrossDesc)]),
+            "llsa_cross_attn_fwd": (ctypes.c_int, [P(LlsaCrossDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                   ctypes.c_size_t, vp, vp]),
+            "llsa_cross_attn_bwd": (ctypes.c_int, [P(LlsaCrossDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                   vp, ctypes.c_size_t, vp, vp]),
             "llsa_selftest_wait_timeout": (ctypes.c_int, [vp, ctypes.c_uint, vp]),
             "llsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "llsa_version": (ctypes.c_int, []),
@@ -173,6 +208,20 @@ def make_desc(B, H, N, D, L, topk, dtype, sm_scale=0.0, level_w=None, flags=0,
 def level_topk(desc: LlsaDesc, l: int) -> int:
     """K_l of a descriptor: the width of I(l)."""
     return desc.topk_l[l] if desc.topk_l[l] > 0 else desc.topk
+
+
+def make_rope(rot_dim, layout=ROPE_HALF, axes=1, base=0.0, scaling=ROPE_SCALE_NONE, factor=0.0, orig_len=0,
+              mscale=0.0, beta_fast=0.0, beta_slow=0.0) -> LlsaRopeDesc:
+    """Fill an llsa_rope_desc; zeros select the defaults (base 10000, factor
+    1, YaRN's betas 32 and 1, mscale 1 or YaRN's 0.1 ln(factor) + 1)."""
+    return LlsaRopeDesc(int(rot_dim), int(layout), int(axes), int(scaling), int(orig_len), float(mscale),
+                        float(base), float(factor), float(beta_fast), float(beta_slow))
+
+
+def make_cross(B, H, Hkv, N, S, D, dtype, sm_scale=0.0, flags=0) -> LlsaCrossDesc:
+    """Fill an llsa_cross_desc: N queries of H heads over S encoder states of
+    Hkv key heads (Hkv divides H)."""
+    return LlsaCrossDesc(B, H, Hkv, N, S, D, dtype, flags, sm_scale)
 
 
 # ------------------------------------------------------------ entry points
@@ -260,6 +309,49 @@ def llsa_selftest_wait_timeout(dev_status, limit_us, stream=0, check=True):
 def llsa_reorder(B, H, img_h, img_w, D, dtype, src, dst, to_zorder, stream=0, check=True):
     """Raster <-> Z-order permutation of the token axis of [B, H, N, D]."""
     st = lib().llsa_reorder(B, H, img_h, img_w, D, dtype, src, dst, 1 if to_zorder else 0, stream)
+    return _check(st) if check else st
+
+
+def llsa_rope_table(rope, rows, pos, table, stream=0, check=True):
+    """The [rows, rot_dim / 2, 2] cosines and sines of positions ``pos`` (int32
+    [rows, axes]; None: the token's index, or its Z-order pixel with 2 axes)."""
+    st = lib().llsa_rope_table(ctypes.byref(rope), rows, pos, table, stream)
+    return _check(st) if check else st
+
+
+def llsa_rope(rope, B, H, N, D, dtype, table, table_rows, q, k, q_out, k_out, adjoint=False, stream=0, check=True):
+    """Rotate q and k (k and k_out may be None); adjoint: the gradients' way back."""
+    st = lib().llsa_rope(ctypes.byref(rope), B, H, N, D, dtype, table, table_rows, q, k, q_out, k_out,
+                         1 if adjoint else 0, stream)
+    return _check(st) if check else st
+
+
+def llsa_rope_pool(desc, rope, table, table_rows, q, k, v, q_out, k_out, pyramid, stream=0, check=True):
+    """llsa_rope of q and k and llsa_pool of the rotated q, k and of v, in one pass."""
+    st = lib().llsa_rope_pool(ctypes.byref(desc), ctypes.byref(rope), table, table_rows, q, k, v, q_out, k_out,
+                              ctypes.byref(pyramid), stream)
+    return _check(st) if check else st
+
+
+def llsa_cross_fwd_workspace_bytes(desc) -> int:
+    return int(lib().llsa_cross_fwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def llsa_cross_bwd_workspace_bytes(desc) -> int:
+    return int(lib().llsa_cross_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def llsa_cross_attn_fwd(desc, q, k, v, kv_len, key_mask, o, o_res, lse, ws, ws_bytes, dev_status=None, stream=0,
+                        check=True):
+    st = lib().llsa_cross_attn_fwd(ctypes.byref(desc), q, k, v, kv_len, key_mask, o, o_res, lse, ws, ws_bytes,
+                                   dev_status, stream)
+    return _check(st) if check else st
+
+
+def llsa_cross_attn_bwd(desc, q, k, v, kv_len, key_mask, o, o_res, lse, dout, dq, dk, dv, ws, ws_bytes,
+                        dev_status=None, stream=0, check=True):
+    st = lib().llsa_cross_attn_bwd(ctypes.byref(desc), q, k, v, kv_len, key_mask, o, o_res, lse, dout, dq, dk, dv,
+                                   ws, ws_bytes, dev_status, stream)
     return _check(st) if check else st
 
 

@@ -35,7 +35,7 @@ def sources() -> list[str]:
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every CUDA source into libllsa.so; returns the library path."""
-    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
+    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "--threads=0",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
            "-I", INCLUDE, "-I", CSRC, "-o", LIB, *sources()]
     if verbose:

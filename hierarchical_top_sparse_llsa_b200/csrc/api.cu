@@ -7,6 +7,7 @@
 
 #include <mutex>
 
+#include "api_common.cuh"
 #include "llsa_internal.cuh"
 
 namespace llsa {
@@ -22,14 +23,16 @@ cudaError_t launch_qkv_pool(const CUtensorMap* maps, void* const out[3], float* 
                             int B, int N, int H, int D, int L, int C, cudaStream_t s);
 }  // namespace llsa
 
-using namespace llsa;
-
 namespace {
 
 // K_l, the width of I(l): topk_l[l], or topk where that is 0.
 inline int k_level(const llsa_desc* d, int l) { return d->topk_l[l] > 0 ? d->topk_l[l] : d->topk; }
 
-inline int check_desc(const llsa_desc* d) {
+}  // namespace
+
+namespace llsa {
+
+int check_desc(const llsa_desc* d) {
   if (d == nullptr) return LLSA_ERR_INVALID_ARG;
   if (d->B < 1 || d->H < 1 || d->N < kBlock || d->D < 1 || d->L < 1 || d->topk < 1)
     return LLSA_ERR_INVALID_ARG;
@@ -53,6 +56,25 @@ inline int check_desc(const llsa_desc* d) {
     if (!(d->level_w[l] >= 0.f) || isinf(d->level_w[l])) return LLSA_ERR_INVALID_ARG;
   return LLSA_OK;
 }
+
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+}  // namespace llsa
+
+using namespace llsa;
+
+namespace {
 
 inline int n_level(const llsa_desc* d, int l) { return d->N >> (4 * l); }
 
@@ -120,25 +142,6 @@ inline TrWsLayout tr_ws_layout(const llsa_desc* d) {
 }
 
 inline int launch_status(cudaError_t e) { return e == cudaSuccess ? LLSA_OK : LLSA_ERR_LAUNCH; }
-
-// cuTensorMapEncodeTiled, fetched from the driver once (no link-time libcuda).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
 
 // A bf16 [rows, D] row-major tensor seen by TMA as tiles of 16 rows x 64
 // columns (128 bytes) with 128-byte swizzle.

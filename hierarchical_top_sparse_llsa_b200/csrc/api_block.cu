@@ -1,0 +1,380 @@
+// Host side of the C ABI's calls around the self-attention: rotary positions
+// and cross attention (argument checks, workspace layouts, dispatch).  No
+// allocation, no state.
+
+#include <math.h>
+#include <string.h>
+
+#include "api_common.cuh"
+#include "cross.cuh"
+#include "llsa_internal.cuh"
+#include "rope.cuh"
+
+using namespace llsa;
+
+namespace {
+
+inline int launch_status(cudaError_t e) { return e == cudaSuccess ? LLSA_OK : LLSA_ERR_LAUNCH; }
+
+inline bool aligned(const void* ptr, size_t n) { return (reinterpret_cast<uintptr_t>(ptr) & (n - 1)) == 0; }
+
+// ----------------------------------------------------------- rotary positions
+int check_rope(const llsa_rope_desc* r) {
+  if (r == nullptr) return LLSA_ERR_INVALID_ARG;
+  if (r->rot_dim < 2 || r->rot_dim % 2 != 0) return LLSA_ERR_INVALID_ARG;
+  if (r->rot_dim > 2 * kMaxRopeFreqs) return LLSA_ERR_UNSUPPORTED;
+  if (r->layout != LLSA_ROPE_HALF && r->layout != LLSA_ROPE_INTERLEAVED) return LLSA_ERR_INVALID_ARG;
+  if ((r->axes != 1 && r->axes != 2) || (r->rot_dim / 2) % r->axes != 0) return LLSA_ERR_INVALID_ARG;
+  if (r->scaling < LLSA_ROPE_SCALE_NONE || r->scaling > LLSA_ROPE_SCALE_YARN) return LLSA_ERR_INVALID_ARG;
+  if (!(r->mscale >= 0.f) || isinf(r->mscale)) return LLSA_ERR_INVALID_ARG;
+  if (r->base != 0.0 && (!(r->base > 1.0) || isinf(r->base))) return LLSA_ERR_INVALID_ARG;
+  if (r->factor != 0.0 && (!(r->factor >= 1.0) || isinf(r->factor))) return LLSA_ERR_INVALID_ARG;
+  if (r->scaling == LLSA_ROPE_SCALE_YARN) {
+    const double fast = r->beta_fast != 0.0 ? r->beta_fast : 32.0, slow = r->beta_slow != 0.0 ? r->beta_slow : 1.0;
+    if (r->orig_len < 1 || !(slow > 0.0) || !(fast > slow) || isinf(fast)) return LLSA_ERR_INVALID_ARG;
+  }
+  return LLSA_OK;
+}
+
+// The frequencies of a checked descriptor, in turns per position.
+RopeFreqs rope_freqs(const llsa_rope_desc* r) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  RopeFreqs f;
+  memset(&f, 0, sizeof(f));
+  f.half = r->rot_dim / 2;
+  f.axes = r->axes;
+  f.n = f.half / f.axes;
+  const double n = (double)f.n;
+  const double factor = r->factor != 0.0 ? r->factor : 1.0;
+  double base = r->base != 0.0 ? r->base : 10000.0;
+  if (r->scaling == LLSA_ROPE_SCALE_NTK && f.n > 1) base *= pow(factor, n / (n - 1.0));
+  double lo = 0.0, hi = 0.0;
+  if (r->scaling == LLSA_ROPE_SCALE_YARN) {
+    const double fast = r->beta_fast != 0.0 ? r->beta_fast : 32.0, slow = r->beta_slow != 0.0 ? r->beta_slow : 1.0;
+    lo = fmax(floor(n * log((double)r->orig_len / (fast * kTwoPi)) / log(base)), 0.0);
+    hi = fmin(ceil(n * log((double)r->orig_len / (slow * kTwoPi)) / log(base)), n - 1.0);
+  }
+  for (int j = 0; j < f.n; ++j) {
+    double w = pow(base, -(double)j / n);
+    if (r->scaling == LLSA_ROPE_SCALE_LINEAR) w /= factor;
+    if (r->scaling == LLSA_ROPE_SCALE_YARN) {
+      const double ramp = fmin(fmax(((double)j - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
+      w = w / factor * ramp + w * (1.0 - ramp);
+    }
+    f.turns[j] = w / kTwoPi;
+  }
+  f.m = r->mscale > 0.f ? r->mscale
+                        : (r->scaling == LLSA_ROPE_SCALE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f);
+  return f;
+}
+
+inline bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + bytes && y < x + bytes;
+}
+
+// Whether each output is its own input or disjoint from every tensor given.
+// in[i] for i < n are inputs, out[i] for i < m the outputs of the first m.
+bool outputs_apart(const void* const* in, int n, void* const* out, int m, size_t bytes) {
+  for (int i = 0; i < m; ++i) {
+    for (int j = 0; j < n; ++j)
+      if (overlap(out[i], in[j], bytes) && !(i == j && out[i] == in[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j], bytes)) return false;
+  }
+  return true;
+}
+
+// A buffer of a call, for the check that outputs overlap nothing.
+struct Span {
+  const void* ptr;
+  size_t bytes;
+};
+
+bool spans_meet(const Span& a, const Span& b) {
+  if (a.ptr == nullptr || b.ptr == nullptr) return false;
+  const uintptr_t x = (uintptr_t)a.ptr, y = (uintptr_t)b.ptr;
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether the first `outs` spans overlap neither each other nor the rest.
+bool spans_apart(const Span* s, int n, int outs) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = 0; j < n; ++j)
+      if (j != i && spans_meet(s[i], s[j])) return false;
+  return true;
+}
+
+RopeParams rope_params(const llsa_rope_desc* r, int B, int H, int N, int D, const float* table, int table_rows) {
+  RopeParams p;
+  memset(&p, 0, sizeof(p));
+  p.table = table;
+  p.B = B;
+  p.H = H;
+  p.N = N;
+  p.D = D;
+  p.rot = r->rot_dim;
+  p.interleaved = r->layout == LLSA_ROPE_INTERLEAVED;
+  p.per_batch = table_rows != N;
+  p.sign = 1.f;
+  return p;
+}
+
+// -------------------------------------------------------------- cross attention
+int check_cross(const llsa_cross_desc* d) {
+  if (d == nullptr) return LLSA_ERR_INVALID_ARG;
+  if (d->B < 1 || d->H < 1 || d->Hkv < 1 || d->N < 1 || d->S < 0 || d->D < 1) return LLSA_ERR_INVALID_ARG;
+  if (d->H % d->Hkv != 0 || d->flags != 0) return LLSA_ERR_INVALID_ARG;
+  if (d->dtype != LLSA_F32 && d->dtype != LLSA_BF16) return LLSA_ERR_INVALID_ARG;
+  if (!(d->sm_scale >= 0.f) || isinf(d->sm_scale)) return LLSA_ERR_INVALID_ARG;
+  if (d->D != 64 && d->D != 128) return LLSA_ERR_UNSUPPORTED;
+  if ((long long)d->B * d->H > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+  if ((long long)d->B * d->H * d->N > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;    // rows are int32
+  if ((long long)d->B * d->Hkv * d->S > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+  return LLSA_OK;
+}
+
+struct CrossWs {
+  CrossPlan plan;
+  size_t delta = 0, a = 0, b = 0, c = 0, total = 0;  // a: O or dQ parts, b: (m, l) or dK parts, c: dV parts
+};
+
+inline size_t take(size_t* off, size_t bytes) {
+  const size_t at = *off;
+  *off += (bytes + 255) & ~(size_t)255;
+  return at;
+}
+
+CrossWs cross_fwd_ws(const llsa_cross_desc* d) {
+  CrossWs w;
+  w.plan = cross_simt_fwd_plan(d);
+  const size_t rows = (size_t)d->B * d->H * d->N;
+  if (w.plan.nks > 1) {
+    w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
+    w.b = take(&w.total, w.plan.nks * rows * sizeof(float2));
+  }
+  return w;
+}
+
+CrossWs cross_bwd_ws(const llsa_cross_desc* d) {
+  CrossWs w;
+  w.plan = cross_simt_bwd_plan(d);
+  const size_t rows = (size_t)d->B * d->H * d->N, keys = (size_t)d->B * d->Hkv * d->S;
+  w.delta = take(&w.total, rows * sizeof(float));
+  if (w.plan.nks > 1) w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
+  if (w.plan.nz > 1) {
+    w.b = take(&w.total, w.plan.nz * keys * d->D * sizeof(float));
+    w.c = take(&w.total, w.plan.nz * keys * d->D * sizeof(float));
+  }
+  return w;
+}
+
+int check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return LLSA_OK;
+  if (ws == nullptr || !aligned(ws, 256)) return LLSA_ERR_INVALID_ARG;
+  return ws_bytes < need ? LLSA_ERR_WORKSPACE : LLSA_OK;
+}
+
+CrossParams cross_params(const llsa_cross_desc* d, const void* q, const void* k, const void* v,
+                         const int32_t* kv_len, const uint8_t* mask, int32_t* status, const CrossPlan& plan) {
+  CrossParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.kv_len = kv_len;
+  p.mask = mask;
+  p.status = status;
+  p.B = d->B;
+  p.H = d->H;
+  p.Hkv = d->Hkv;
+  p.N = d->N;
+  p.S = d->S;
+  p.D = d->D;
+  p.nks = plan.nks;
+  p.nz = plan.nz;
+  p.scale = d->sm_scale > 0.f ? d->sm_scale : 1.0f / sqrtf((float)d->D);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int llsa_rope_table(const llsa_rope_desc* rope, int rows, const int32_t* pos, float* table, void* stream) {
+  const int st = check_rope(rope);
+  if (st != LLSA_OK) return st;
+  if (rows < 1 || table == nullptr || !aligned(table, 16) || !aligned(pos, 4)) return LLSA_ERR_INVALID_ARG;
+  return launch_status(launch_rope_table(rope_freqs(rope), rows, pos, table, (cudaStream_t)stream));
+}
+
+int llsa_rope(const llsa_rope_desc* rope, int B, int H, int N, int D, int dtype, const float* table, int table_rows,
+              const void* q, const void* k, void* q_out, void* k_out, int adjoint, void* stream) {
+  const int st = check_rope(rope);
+  if (st != LLSA_OK) return st;
+  if (B < 1 || H < 1 || N < 1 || D < 1) return LLSA_ERR_INVALID_ARG;
+  if (dtype != LLSA_F32 && dtype != LLSA_BF16) return LLSA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return LLSA_ERR_UNSUPPORTED;
+  if ((long long)H * 2 > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+  if (rope->rot_dim > D) return LLSA_ERR_INVALID_ARG;
+  if (table == nullptr || q == nullptr || q_out == nullptr || (k == nullptr) != (k_out == nullptr))
+    return LLSA_ERR_INVALID_ARG;
+  if (table_rows != N && (long long)table_rows != (long long)B * N) return LLSA_ERR_INVALID_ARG;
+  if (!aligned(table, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
+    return LLSA_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)B * H * N * D * (dtype == LLSA_BF16 ? 2 : 4);
+  const int nt = k != nullptr ? 2 : 1;
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  if (!outputs_apart(in, nt, out, nt, bytes)) return LLSA_ERR_INVALID_ARG;
+  RopeParams p = rope_params(rope, B, H, N, D, table, table_rows);
+  for (int t = 0; t < nt; ++t) {
+    p.x[t] = in[t];
+    p.y[t] = out[t];
+  }
+  p.ntensor = nt;
+  p.sign = adjoint != 0 ? -1.f : 1.f;
+  return launch_status(launch_rope(p, dtype, (cudaStream_t)stream));
+}
+
+int llsa_rope_pool(const llsa_desc* desc, const llsa_rope_desc* rope, const float* table, int table_rows,
+                   const void* q, const void* k, const void* v, void* q_out, void* k_out, const llsa_pyramid* out,
+                   void* stream) {
+  int st = check_desc(desc);
+  if (st == LLSA_OK) st = check_rope(rope);
+  if (st != LLSA_OK) return st;
+  if (rope->rot_dim > desc->D) return LLSA_ERR_INVALID_ARG;
+  if (table == nullptr || q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || k_out == nullptr ||
+      out == nullptr)
+    return LLSA_ERR_INVALID_ARG;
+  if (table_rows != desc->N && (long long)table_rows != (long long)desc->B * desc->N) return LLSA_ERR_INVALID_ARG;
+  const void* all[6] = {table, q, k, v, q_out, k_out};
+  for (const void* ptr : all)
+    if (!aligned(ptr, 16)) return LLSA_ERR_INVALID_ARG;
+  for (int l = 1; l <= desc->L; ++l) {
+    if (out->q[l] == nullptr || out->k[l] == nullptr) return LLSA_ERR_INVALID_ARG;
+    if (l >= 2 && out->v[l] == nullptr) return LLSA_ERR_INVALID_ARG;
+    if (!aligned(out->q[l], 16) || !aligned(out->k[l], 16)) return LLSA_ERR_INVALID_ARG;
+  }
+  const size_t bytes = (size_t)desc->B * desc->H * desc->N * desc->D * (desc->dtype == LLSA_BF16 ? 2 : 4);
+  const void* in[3] = {q, k, v};
+  void* rot[2] = {q_out, k_out};
+  if (!outputs_apart(in, 3, rot, 2, bytes)) return LLSA_ERR_INVALID_ARG;
+  RopeParams p = rope_params(rope, desc->B, desc->H, desc->N, desc->D, table, table_rows);
+  PoolParams o;
+  memset(&o, 0, sizeof(o));
+  for (int t = 0; t < 3; ++t) p.x[t] = in[t];
+  for (int t = 0; t < 2; ++t) p.y[t] = rot[t];
+  p.ntensor = 2;
+  for (int l = 1; l <= desc->L; ++l) {
+    o.lvl[0][l] = out->q[l];
+    o.lvl[1][l] = out->k[l];
+    o.lvl[2][l] = l >= 2 ? out->v[l] : nullptr;
+  }
+  o.BH = desc->B * desc->H;
+  o.N = desc->N;
+  o.D = desc->D;
+  o.L = desc->L;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (rope_pool_fused(rope->rot_dim, p.interleaved != 0, desc->dtype))
+    return launch_status(launch_rope_pool(p, o, desc->dtype, s));
+  // pairs that straddle the 16-byte chunks: the two calls one after the other
+  const cudaError_t e = launch_rope(p, desc->dtype, s);
+  if (e != cudaSuccess) return LLSA_ERR_LAUNCH;
+  o.x[0] = q_out;
+  o.x[1] = k_out;
+  o.x[2] = v;
+  return launch_status(launch_pool(o, desc->dtype, s));
+}
+
+size_t llsa_cross_fwd_workspace_bytes(const llsa_cross_desc* desc) {
+  return check_cross(desc) == LLSA_OK ? cross_fwd_ws(desc).total : 0;
+}
+
+size_t llsa_cross_bwd_workspace_bytes(const llsa_cross_desc* desc) {
+  return check_cross(desc) == LLSA_OK ? cross_bwd_ws(desc).total : 0;
+}
+
+int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, const void* k, const void* v,
+                        const int32_t* kv_len, const uint8_t* key_mask, void* o, void* o_res, float* lse, void* ws,
+                        size_t ws_bytes, int32_t* dev_status, void* stream) {
+  int st = check_cross(desc);
+  if (st != LLSA_OK) return st;
+  if (q == nullptr || o == nullptr || lse == nullptr) return LLSA_ERR_INVALID_ARG;
+  if (desc->S > 0 && (k == nullptr || v == nullptr)) return LLSA_ERR_INVALID_ARG;
+  const void* ptrs[5] = {q, k, v, o, o_res};
+  for (const void* ptr : ptrs)
+    if (!aligned(ptr, 16)) return LLSA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(kv_len, 4)) return LLSA_ERR_INVALID_ARG;
+  const CrossWs w = cross_fwd_ws(desc);
+  st = check_ws(ws, ws_bytes, w.total);
+  if (st != LLSA_OK) return st;
+  const size_t e = desc->dtype == LLSA_BF16 ? 2 : 4, rows = (size_t)desc->B * desc->H * desc->N;
+  const size_t qb = rows * desc->D * e, kb = (size_t)desc->B * desc->Hkv * desc->S * desc->D * e;
+  const Span spans[] = {{o, qb}, {desc->dtype == LLSA_BF16 ? o_res : nullptr, qb}, {lse, rows * 4}, {ws, w.total},
+                        {q, qb}, {k, kb}, {v, kb}, {kv_len, (size_t)desc->B * 4}, {key_mask, (size_t)desc->B * desc->S}};
+  if (!spans_apart(spans, 9, 4)) return LLSA_ERR_INVALID_ARG;
+  CrossParams p = cross_params(desc, q, k, v, kv_len, key_mask, dev_status, w.plan);
+  p.o = o;
+  p.o_res = desc->dtype == LLSA_BF16 ? o_res : nullptr;
+  p.lse = lse;
+  char* base = static_cast<char*>(ws);
+  if (p.nks > 1) {
+    p.part_o = reinterpret_cast<float*>(base + w.a);
+    p.part_ml = reinterpret_cast<float2*>(base + w.b);
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t err = launch_cross_fwd_simt(p, desc->dtype, s);
+  if (err == cudaSuccess && p.nks > 1) err = launch_cross_combine(p, desc->dtype, s);
+  return launch_status(err);
+}
+
+int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* k, const void* v,
+                        const int32_t* kv_len, const uint8_t* key_mask, const void* o, const void* o_res,
+                        const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                        int32_t* dev_status, void* stream) {
+  int st = check_cross(desc);
+  if (st != LLSA_OK) return st;
+  if (q == nullptr || o == nullptr || lse == nullptr || dout == nullptr || dq == nullptr) return LLSA_ERR_INVALID_ARG;
+  if (desc->S > 0 && (k == nullptr || v == nullptr || dk == nullptr || dv == nullptr)) return LLSA_ERR_INVALID_ARG;
+  const void* ptrs[9] = {q, k, v, o, o_res, dout, dq, dk, dv};
+  for (const void* ptr : ptrs)
+    if (!aligned(ptr, 16)) return LLSA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(kv_len, 4)) return LLSA_ERR_INVALID_ARG;
+  const CrossWs w = cross_bwd_ws(desc);
+  st = check_ws(ws, ws_bytes, w.total);
+  if (st != LLSA_OK) return st;
+  const size_t rows = (size_t)desc->B * desc->H * desc->N, keys = (size_t)desc->B * desc->Hkv * desc->S;
+  const size_t item = desc->dtype == LLSA_BF16 ? 2 : 4, qb = rows * desc->D * item, kb = keys * desc->D * item;
+  const Span spans[] = {{dq, qb}, {dk, kb}, {dv, kb}, {ws, w.total}, {q, qb}, {k, kb}, {v, kb}, {o, qb},
+                        {desc->dtype == LLSA_BF16 ? o_res : nullptr, qb}, {lse, rows * 4}, {dout, qb},
+                        {kv_len, (size_t)desc->B * 4}, {key_mask, (size_t)desc->B * desc->S}};
+  if (!spans_apart(spans, 13, 4)) return LLSA_ERR_INVALID_ARG;
+  CrossParams p = cross_params(desc, q, k, v, kv_len, key_mask, dev_status, w.plan);
+  p.o_in = o;
+  p.res_in = desc->dtype == LLSA_BF16 ? o_res : nullptr;
+  p.lse_in = lse;
+  p.dout = dout;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  char* base = static_cast<char*>(ws);
+  p.delta = reinterpret_cast<float*>(base + w.delta);
+  if (p.nks > 1) p.part_dq = reinterpret_cast<float*>(base + w.a);
+  if (p.nz > 1) {
+    p.part_dk = reinterpret_cast<float*>(base + w.b);
+    p.part_dv = reinterpret_cast<float*>(base + w.c);
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = launch_cross_delta(p, desc->dtype, s);
+  if (e == cudaSuccess) e = launch_cross_bwd_simt(p, desc->dtype, s);
+  if (e == cudaSuccess && p.nks > 1)
+    e = launch_cross_reduce(p.part_dq, dq, p.nks, rows * p.D, p.scale, desc->dtype, s);
+  if (e == cudaSuccess && p.nz > 1) {
+    e = launch_cross_reduce(p.part_dk, dk, p.nz, keys * p.D, p.scale, desc->dtype, s);
+    if (e == cudaSuccess) e = launch_cross_reduce(p.part_dv, dv, p.nz, keys * p.D, 1.f, desc->dtype, s);
+  }
+  return launch_status(e);
+}
+
+}  // extern "C"

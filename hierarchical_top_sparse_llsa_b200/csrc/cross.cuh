@@ -1,0 +1,58 @@
+// Launch parameters of the cross-attention kernels (not part of the C ABI).
+#pragma once
+
+#include "llsa_internal.cuh"
+
+namespace llsa {
+
+struct CrossParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* kv_len;   // [B] or null
+  const uint8_t* mask;     // [B, S] or null
+  const void* o_in;        // bwd: O
+  const void* res_in;      // bwd: bf16 residual of O or null
+  const float* lse_in;     // bwd
+  const void* dout;
+  void* o;
+  void* o_res;
+  float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* part_o;   // fwd, nks > 1: [nks][B H N][D], the splits' unnormalised O
+  float2* part_ml; // fwd, nks > 1: [nks][B H N], their maxima (base 2) and sums
+  float* delta;    // bwd: [B H N]
+  float* part_dq;  // bwd, nks > 1: [nks][B H N][D]
+  float* part_dk;  // bwd, nz > 1: [nz][B Hkv S][D]
+  float* part_dv;
+  int32_t* status;
+  int B, H, Hkv, N, S, D;
+  int nks;         // splits of the keys (fwd: of O; bwd: of dQ)
+  int nz;          // bwd: segments of the query tiles (dK, dV)
+  float scale;
+};
+
+// Key tokens that batch entry b sees at the front (the mask aside).
+__device__ __forceinline__ int cross_len(const CrossParams& p, int b) {
+  if (p.kv_len == nullptr) return p.S;
+  const int n = p.kv_len[b];
+  return n < 0 ? 0 : (n > p.S ? p.S : n);
+}
+
+// How the work is cut, from the sizes alone (workspace sizes follow from it).
+struct CrossPlan {
+  int nks, nz;
+};
+CrossPlan cross_simt_fwd_plan(const llsa_cross_desc* d);
+CrossPlan cross_simt_bwd_plan(const llsa_cross_desc* d);
+
+cudaError_t launch_cross_fwd_simt(const CrossParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cross_bwd_simt(const CrossParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cross_combine(const CrossParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cross_delta(const CrossParams& p, int dtype, cudaStream_t s);
+// out[i] = f * sum over z < n of part[z][i], i < total (a multiple of 8)
+cudaError_t launch_cross_reduce(const float* part, void* out, int n, size_t total, float f, int dtype, cudaStream_t s);
+
+}  // namespace llsa

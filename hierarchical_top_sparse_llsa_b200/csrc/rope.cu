@@ -1,0 +1,396 @@
+// Rotary positions: the cosine/sine table, the rotation of Q and K (and its
+// adjoint for dQ and dK), and the rotation with the hierarchical compression
+// (Step 1 of the howistudyai explainer of "Trainable Log-linear Sparse
+// Attention for Efficient Diffusion Transformers") of the rotated tensors.
+//
+// A pair (a, b) of a head's channels turns by its token's angle:
+//   (a c - b s, b c + a s)         adjoint: (a c + b s, b c - a s)
+// Products and sums are rounded one by one in fp32 (no FMA), then once to the
+// stored type, so the fused and the separate calls agree bit for bit.
+//
+// All three kernels are bound by memory.  The rotation reads and writes each
+// element once; the table (rot_dim / 2 pairs of fp32, twice a bf16 head row)
+// would be as much traffic again if it were read per head, so a thread keeps
+// the cosines and sines of its token and channels in registers and walks the
+// heads of Q and K with them.
+
+#include "llsa_internal.cuh"
+#include "rope.cuh"
+
+namespace llsa {
+
+namespace {
+
+constexpr int kSms = 148;
+
+// ---------------------------------------------------------------- the table
+constexpr int kTableThreads = 256;
+
+// the low 32 bits' even-position bits packed into the low 16 (bit 2b -> bit b)
+__device__ __forceinline__ uint32_t even_bits(uint32_t v) {
+  v &= 0x55555555u;
+  v = (v | (v >> 1)) & 0x33333333u;
+  v = (v | (v >> 2)) & 0x0f0f0f0fu;
+  v = (v | (v >> 4)) & 0x00ff00ffu;
+  v = (v | (v >> 8)) & 0x0000ffffu;
+  return v;
+}
+
+// Thread (r, j): pairs 2 j and 2 j + 1 of rows r, r + step, ...  The angle is
+// held in turns: position * (f / 2 pi) in fp64, its whole turns taken off
+// exactly (x - rint(x) is exact), and only the remainder in [-1/2, 1/2] is
+// rounded to fp32 (sincospi of twice it), so the angle's error is 2^-53 of the
+// turns made plus 2^-24 of a half turn at any position.
+__global__ void __launch_bounds__(kTableThreads)
+rope_table_kernel(RopeFreqs f, int rows, const int32_t* __restrict__ pos, float* __restrict__ table) {
+  const int hp = (f.half + 1) / 2;  // threads per row
+  const int per = kTableThreads / hp;
+  const int r0 = threadIdx.x / hp, j = threadIdx.x % hp;
+  if (r0 >= per) return;
+  const int p0 = 2 * j, p1 = min(2 * j + 1, f.half - 1);  // a lone last pair is computed twice
+  const int a0 = p0 / f.n, a1 = p1 / f.n;
+  const double f0 = f.turns[p0 % f.n], f1 = f.turns[p1 % f.n];
+  for (long long r = (long long)blockIdx.x * per + r0; r < rows; r += (long long)gridDim.x * per) {
+    int x0, x1;
+    if (pos != nullptr) {
+      x0 = pos[r * f.axes + a0];
+      x1 = pos[r * f.axes + a1];
+    } else if (f.axes == 1) {
+      x0 = x1 = (int)r;
+    } else {
+      const int x = (int)even_bits((uint32_t)r), y = (int)even_bits((uint32_t)r >> 1);
+      x0 = a0 ? y : x;
+      x1 = a1 ? y : x;
+    }
+    const double t0 = (double)x0 * f0, t1 = (double)x1 * f1;
+    float s0, c0, s1, c1;
+    sincospif(2.0f * (float)(t0 - rint(t0)), &s0, &c0);
+    sincospif(2.0f * (float)(t1 - rint(t1)), &s1, &c1);
+    float* dst = table + (r * f.half + p0) * 2;
+    if ((f.half & 1) == 0) {  // whole rows are 16-byte aligned
+      *reinterpret_cast<float4*>(dst) = make_float4(c0 * f.m, s0 * f.m, c1 * f.m, s1 * f.m);
+    } else {
+      *reinterpret_cast<float2*>(dst) = make_float2(c0 * f.m, s0 * f.m);
+      if (p0 + 1 < f.half) *reinterpret_cast<float2*>(dst + 2) = make_float2(c1 * f.m, s1 * f.m);
+    }
+  }
+}
+
+// ------------------------------------------------------------- the rotation
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* v);
+template <>
+__device__ __forceinline__ uint4 pack16<float>(const float* v) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+template <>
+__device__ __forceinline__ uint4 pack16<bf16>(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A slot is two 16-byte chunks of a head row that hold whole pairs: in the
+// interleaved layout chunks 2 s and 2 s + 1, in the half layout chunk s and
+// its partner rot_dim / 2 channels on (or, past the rotated channels, two
+// neighbouring ones).  Needs rot_dim / 2 to be a multiple of a chunk in the
+// half layout.
+template <typename T>
+struct Slot {
+  static constexpr int VEC = Vec16<T>::N;
+  int c0, c1;  // its chunks
+  int pair0;   // its first pair
+  int nrot;    // how many of its VEC pairs turn
+  __device__ __forceinline__ Slot(int s, int half, bool interleaved) {
+    if (interleaved) {
+      c0 = 2 * s;
+      c1 = 2 * s + 1;
+      pair0 = s * VEC;
+      nrot = min(max(half - pair0, 0), VEC);
+    } else {
+      const int hc = half / VEC;  // chunks of the first half
+      const bool rot = s < hc;
+      c0 = rot ? s : 2 * s;
+      c1 = rot ? s + hc : 2 * s + 1;
+      pair0 = rot ? s * VEC : 0;
+      nrot = rot ? VEC : 0;
+    }
+  }
+};
+
+// cosines and sines of a slot's pairs (those that do not turn are not read)
+template <int VEC>
+__device__ __forceinline__ void load_turns(const float* __restrict__ row, int pair0, int nrot, float sign, float* c,
+                                           float* s) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    float2 t = make_float2(1.f, 0.f);
+    if (e < nrot) t = __ldg(reinterpret_cast<const float2*>(row) + pair0 + e);
+    c[e] = t.x;
+    s[e] = sign * t.y;
+  }
+}
+
+// The slot's two chunks, turned; what does not turn keeps its bits.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void turn_slot(uint4 (&v)[2], const float* c, const float* s, int nrot) {
+  constexpr int VEC = Vec16<T>::N;
+  float x[2 * VEC];
+  Vec16<T>::unpack(v[0], x);
+  Vec16<T>::unpack(v[1], x + VEC);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    if (kInterleaved) turn(x[2 * e], x[2 * e + 1], c[e], s[e]);
+    else turn(x[e], x[VEC + e], c[e], s[e]);
+  }
+  // word i of the two chunks belongs to pair i VEC / 8 (in the half layout a
+  // slot turns as a whole or not at all)
+  const uint4 w0 = pack16<T>(x), w1 = pack16<T>(x + VEC);
+  if (0 * VEC / 8 < nrot) v[0].x = w0.x;
+  if (1 * VEC / 8 < nrot) v[0].y = w0.y;
+  if (2 * VEC / 8 < nrot) v[0].z = w0.z;
+  if (3 * VEC / 8 < nrot) v[0].w = w0.w;
+  if (4 * VEC / 8 < nrot) v[1].x = w1.x;
+  if (5 * VEC / 8 < nrot) v[1].y = w1.y;
+  if (6 * VEC / 8 < nrot) v[1].z = w1.z;
+  if (7 * VEC / 8 < nrot) v[1].w = w1.w;
+}
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;
+
+// Thread: one slot of one token, over `per` of the (tensor, head) rows that
+// share the token's table row.  Every element is read and written by one
+// thread, the reads first, so the outputs may be the inputs.
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(RopeParams p) {
+  constexpr int VEC = Vec16<T>::N;
+  const int slots = p.D / (2 * VEC);
+  const int half = p.rot / 2;
+  const long long e = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  const long long tok = e / slots;  // b * N + n
+  if (tok >= (long long)p.B * p.N) return;
+  const long long b = tok / p.N, n = tok - b * p.N;
+  const Slot<T> sl((int)(e - tok * slots), half, kInterleaved);
+  float c[VEC], s[VEC];
+  load_turns<VEC>(p.table + (p.per_batch ? tok : n) * (2 * half), sl.pair0, sl.nrot, p.sign, c, s);
+  const int rows = p.H * p.ntensor;
+  const int i0 = blockIdx.y * p.per, i1 = min(rows, i0 + p.per);
+  for (int i = i0; i < i1; i += kRopeUnroll) {
+    uint4 v[kRopeUnroll][2];
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      if (i + u < i1) {
+        const int t = (i + u) / p.H, h = (i + u) - t * p.H;
+        const uint4* src = static_cast<const uint4*>(p.x[t]) + ((b * p.H + h) * p.N + n) * (p.D / VEC);
+        v[u][0] = src[sl.c0];
+        v[u][1] = src[sl.c1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      if (i + u < i1) {
+        const int t = (i + u) / p.H, h = (i + u) - t * p.H;
+        uint4* dst = static_cast<uint4*>(p.y[t]) + ((b * p.H + h) * p.N + n) * (p.D / VEC);
+        turn_slot<T, kInterleaved>(v[u], c, s, sl.nrot);
+        dst[sl.c0] = v[u][0];
+        dst[sl.c1] = v[u][1];
+      }
+    }
+  }
+}
+
+// The half layout where a partner sits off the 16-byte chunks: a thread per
+// pair (or per two channels that pass through), element by element.
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_ragged_kernel(RopeParams p) {
+  const int half = p.rot / 2, slots = p.D / 2;
+  const long long e = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  const long long tok = e / slots;
+  if (tok >= (long long)p.B * p.N) return;
+  const long long b = tok / p.N, n = tok - b * p.N;
+  const int s = (int)(e - tok * slots);
+  const bool rot = s < half;
+  const int d0 = rot ? s : 2 * s, d1 = rot ? s + half : 2 * s + 1;
+  float2 t = make_float2(1.f, 0.f);
+  if (rot) t = __ldg(reinterpret_cast<const float2*>(p.table + (p.per_batch ? tok : n) * (2 * half)) + s);
+  t.y *= p.sign;
+  const int rows = p.H * p.ntensor;
+  const int i1 = min(rows, (int)(blockIdx.y + 1) * p.per);
+  for (int i = blockIdx.y * p.per; i < i1; ++i) {
+    const int k = i / p.H, h = i - k * p.H;
+    const long long row = ((b * p.H + h) * p.N + n) * p.D;
+    const T* src = static_cast<const T*>(p.x[k]) + row;
+    T* dst = static_cast<T*>(p.y[k]) + row;
+    if (rot) {
+      float x = to_f32(src[d0]), y = to_f32(src[d1]);
+      turn(x, y, t.x, t.y);
+      store_elem(dst + d0, x);
+      store_elem(dst + d1, y);
+    } else {
+      const T x = src[d0], y = src[d1];
+      dst[d0] = x;
+      dst[d1] = y;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_rope_typed(RopeParams p, cudaStream_t s) {
+  const int half = p.rot / 2;
+  constexpr int VEC = Vec16<T>::N;
+  const bool ragged = !p.interleaved && half % VEC != 0;
+  const int slots = ragged ? p.D / 2 : p.D / (2 * VEC);
+  const long long threads = (long long)p.B * p.N * slots;
+  const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // rows a thread walks: all that share its table row, fewer when that leaves
+  // the SMs (8 blocks each) without work
+  const int rows = p.H * p.ntensor;
+  const long long want = 8LL * kSms;
+  long long parts = (want + blocks - 1) / blocks;
+  if (parts > rows) parts = rows;
+  if (parts < (rows + 65534) / 65535) parts = (rows + 65534) / 65535;
+  p.per = (int)((rows + parts - 1) / parts);
+  const dim3 grid((unsigned)blocks, (unsigned)((rows + p.per - 1) / p.per));
+  if (ragged) rope_ragged_kernel<T><<<grid, kRopeThreads, 0, s>>>(p);
+  else if (p.interleaved) rope_kernel<T, true><<<grid, kRopeThreads, 0, s>>>(p);
+  else rope_kernel<T, false><<<grid, kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------ the rotation with the pool
+// One CTA: 256 tokens of one (b, h) of one tensor; thread (t1, slot) turns and
+// sums the 16 rows of level-1 token t1 (16 rows of two chunks), left to right,
+// as the pool kernel does; level 2 from the level-1 means in shared memory.
+// The tensors and heads that share a table row run next to each other.
+constexpr int kPoolRows = 4;  // rows in flight per thread
+
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(16 * D / (2 * Vec16<T>::N))
+rope_pool_kernel(RopeParams p, PoolParams o) {
+  constexpr int VEC = Vec16<T>::N;
+  constexpr int SL = D / (2 * VEC);  // slots per row
+  __shared__ __align__(16) float m1[16][D];
+  const int nt = o.L >= 2 ? 3 : 2;  // V has no level-1 output
+  long long id = blockIdx.x;
+  const int tensor = (int)(id % nt);
+  id /= nt;
+  const int bh = (int)(id % o.BH);
+  const int chunk = (int)(id / o.BH);
+  const int t1 = threadIdx.x / SL;
+  const int n1 = o.N / kBlock;
+  const int g1 = chunk * 16 + t1;
+  const int half = p.rot / 2;
+  const Slot<T> sl(threadIdx.x % SL, half, kInterleaved);
+  const int nrot = tensor < 2 ? sl.nrot : 0;
+  if (g1 < n1) {
+    const size_t row0 = (size_t)bh * o.N + (size_t)g1 * kBlock;
+    const uint4* src = static_cast<const uint4*>(p.x[tensor]) + row0 * (D / VEC);
+    uint4* dst = tensor < 2 ? static_cast<uint4*>(p.y[tensor]) + row0 * (D / VEC) : nullptr;
+    const size_t trow = (p.per_batch ? (size_t)(bh / p.H) * o.N : 0) + (size_t)g1 * kBlock;
+    const float* tab = p.table + trow * (2 * half);
+    float acc[2 * VEC];
+#pragma unroll
+    for (int j0 = 0; j0 < kBlock; j0 += kPoolRows) {
+      uint4 v[kPoolRows][2];
+#pragma unroll
+      for (int j = 0; j < kPoolRows; ++j) {
+        v[j][0] = src[(j0 + j) * (D / VEC) + sl.c0];
+        v[j][1] = src[(j0 + j) * (D / VEC) + sl.c1];
+      }
+#pragma unroll
+      for (int j = 0; j < kPoolRows; ++j) {
+        if (tensor < 2) {
+          float c[VEC], s[VEC];
+          load_turns<VEC>(tab + (size_t)(j0 + j) * (2 * half), sl.pair0, nrot, 1.f, c, s);
+          turn_slot<T, kInterleaved>(v[j], c, s, nrot);
+          dst[(j0 + j) * (D / VEC) + sl.c0] = v[j][0];
+          dst[(j0 + j) * (D / VEC) + sl.c1] = v[j][1];
+        }
+        float x[2 * VEC];  // the means are of the stored values
+        Vec16<T>::unpack(v[j][0], x);
+        Vec16<T>::unpack(v[j][1], x + VEC);
+#pragma unroll
+        for (int e = 0; e < 2 * VEC; ++e) acc[e] = (j0 + j == 0) ? x[e] : __fadd_rn(acc[e], x[e]);
+      }
+    }
+    float* o1 = o.lvl[tensor][1];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int d = (w ? sl.c1 : sl.c0) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        float4 m;
+        m.x = __fmul_rn(acc[w * VEC + e], 0.0625f);
+        m.y = __fmul_rn(acc[w * VEC + e + 1], 0.0625f);
+        m.z = __fmul_rn(acc[w * VEC + e + 2], 0.0625f);
+        m.w = __fmul_rn(acc[w * VEC + e + 3], 0.0625f);
+        *reinterpret_cast<float4*>(&m1[t1][d + e]) = m;
+        if (o1 != nullptr) *reinterpret_cast<float4*>(o1 + ((size_t)bh * n1 + g1) * D + d + e) = m;
+      }
+    }
+  }
+  if (o.L < 2) return;
+  __syncthreads();
+  // level 2: one level-2 token per CTA (N is a multiple of 256 when L >= 2)
+  for (int d = threadIdx.x; d < D; d += blockDim.x) {
+    float a = m1[0][d];
+#pragma unroll
+    for (int t = 1; t < 16; ++t) a = __fadd_rn(a, m1[t][d]);
+    o.lvl[tensor][2][((size_t)bh * (o.N >> 8) + chunk) * D + d] = __fmul_rn(a, 0.0625f);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_rope_pool_typed(const RopeParams& p, const PoolParams& o, cudaStream_t s) {
+  constexpr int threads = 16 * D / (2 * Vec16<T>::N);
+  const int n1 = o.N / kBlock;
+  const long long blocks = (long long)((n1 + 15) / 16) * o.BH * (o.L >= 2 ? 3 : 2);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (p.interleaved) rope_pool_kernel<T, D, true><<<(unsigned)blocks, threads, 0, s>>>(p, o);
+  else rope_pool_kernel<T, D, false><<<(unsigned)blocks, threads, 0, s>>>(p, o);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeFreqs& f, int rows, const int32_t* pos, float* table, cudaStream_t s) {
+  const int per = kTableThreads / ((f.half + 1) / 2);
+  long long blocks = ((long long)rows + per - 1) / per;
+  if (blocks > 16LL * kSms) blocks = 16LL * kSms;
+  rope_table_kernel<<<(int)blocks, kTableThreads, 0, s>>>(f, rows, pos, table);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope(const RopeParams& p, int dtype, cudaStream_t s) {
+  return dtype == LLSA_BF16 ? launch_rope_typed<bf16>(p, s) : launch_rope_typed<float>(p, s);
+}
+
+bool rope_pool_fused(int rot, bool interleaved, int dtype) {
+  return interleaved || (rot / 2) % (dtype == LLSA_BF16 ? 8 : 4) == 0;
+}
+
+cudaError_t launch_rope_pool(const RopeParams& p, const PoolParams& o, int dtype, cudaStream_t s) {
+  cudaError_t e;
+  if (dtype == LLSA_BF16)
+    e = o.D == 64 ? launch_rope_pool_typed<bf16, 64>(p, o, s) : launch_rope_pool_typed<bf16, 128>(p, o, s);
+  else
+    e = o.D == 64 ? launch_rope_pool_typed<float, 64>(p, o, s) : launch_rope_pool_typed<float, 128>(p, o, s);
+  if (e != cudaSuccess) return e;
+  return launch_pool_up(o, s);
+}
+
+}  // namespace llsa

@@ -358,6 +358,170 @@ LLSA_API int llsa_attn_bwd_noalloc(const llsa_desc* desc, const void* q, const v
 LLSA_API int llsa_reorder(int B, int H, int img_h, int img_w, int D, int dtype, const void* src, void* dst,
                           int to_zorder, void* stream);
 
+/* ------------------------------------------------------ rotary positions
+ *
+ * Positions enter the self-attention by rotating pairs of channels of Q and K
+ * by position-dependent angles before the pooling (the pages' pipeline takes
+ * Q, K, V as given; rotary positions are what diffusion transformers put in
+ * front of it).  A head's first rot_dim channels form rot_dim / 2 pairs, the
+ * others pass through:
+ *   LLSA_ROPE_HALF          pair i is channels (i, i + rot_dim / 2)
+ *   LLSA_ROPE_INTERLEAVED   pair i is channels (2 i, 2 i + 1)
+ *   (a, b) -> (a c - b s, b c + a s),   c, s = m cos(t), m sin(t)
+ * The pairs are shared out over `axes` position axes, n = rot_dim / 2 / axes
+ * each: pair i turns with axis i / n, by the angle
+ *   t = position[axis] * f_(i mod n),   f_j = base^(-j / n)
+ * with f scaled for contexts longer than the trained one:
+ *   LLSA_ROPE_SCALE_NONE     as above
+ *   LLSA_ROPE_SCALE_LINEAR   f_j / factor
+ *   LLSA_ROPE_SCALE_NTK      base replaced by base * factor^(n / (n - 1)) (n > 1)
+ *   LLSA_ROPE_SCALE_YARN     f_j / factor * r_j + f_j * (1 - r_j), with
+ *                            r_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1),
+ *                            lo = max(floor(x(beta_fast)), 0),
+ *                            hi = min(ceil(x(beta_slow)), n - 1),
+ *                            x(beta) = n ln(orig_len / (2 pi beta)) / ln(base)
+ */
+enum { LLSA_ROPE_HALF = 0, LLSA_ROPE_INTERLEAVED = 1 };
+enum {
+  LLSA_ROPE_SCALE_NONE = 0,
+  LLSA_ROPE_SCALE_LINEAR = 1,
+  LLSA_ROPE_SCALE_NTK = 2,
+  LLSA_ROPE_SCALE_YARN = 3
+};
+
+/* How positions rotate (plain data, read before launch). */
+typedef struct {
+  int rot_dim;      /* rotated channels of a head: even, 2 <= rot_dim <= D */
+  int layout;       /* LLSA_ROPE_HALF or LLSA_ROPE_INTERLEAVED */
+  int axes;         /* position axes, 1 or 2; rot_dim / 2 is a multiple of it */
+  int scaling;      /* LLSA_ROPE_SCALE_* */
+  int orig_len;     /* YARN: the trained context length, >= 1; else ignored */
+  float mscale;     /* m, multiplies cosine and sine; 0 selects 1 (YARN: 0.1 ln(factor) + 1) */
+  double base;      /* > 1; 0 selects 10000 */
+  double factor;    /* context stretch, >= 1; 0 selects 1 */
+  double beta_fast; /* YARN: turns within orig_len from which a pair keeps its frequency; 0 selects 32 */
+  double beta_slow; /* YARN: turns below which a pair is fully stretched, < beta_fast; 0 selects 1 */
+} llsa_rope_desc;
+
+/*
+ * llsa_rope_table - the cosines and sines that llsa_rope and llsa_rope_pool
+ * read.  A program builds it once for its positions and keeps it.
+ *   table: fp32 [rows, rot_dim / 2, 2] (cosine, sine of each pair), 16-byte
+ *   aligned, written.  Angles are formed and reduced in fp64, so positions
+ *   far into a context lose nothing; each entry is within 2^-22 m of the
+ *   exact value.
+ *   pos: int32 [rows, axes], any values, or NULL: row r is token r, whose
+ *   position is r (axes = 1) or its pixel (x, y) in Z-order (axes = 2; axis 0
+ *   is x, from the even bits of r, axis 1 is y, from the odd bits).
+ *   rows >= 1.  The layout and D play no part in the table.
+ */
+LLSA_API int llsa_rope_table(const llsa_rope_desc* rope, int rows, const int32_t* pos, float* table, void* stream);
+
+/*
+ * llsa_rope - rotate Q and K (the step between the projection and llsa_pool),
+ * or, with adjoint nonzero, apply the transposed rotation (a c + b s,
+ * b c - a s): the backward, which takes dQ and dK of llsa_attn_bwd to the
+ * gradients of the unrotated tensors.
+ *   q, k: [B, H, N, D] of dtype; k and k_out may both be NULL (one tensor).
+ *   q_out, k_out: written; each may be its own input (in place), otherwise
+ *   outputs overlap nothing (else LLSA_ERR_INVALID_ARG).  D in {64, 128}; B,
+ *   H, N >= 1, N any length.  16-byte aligned.
+ *   table: from llsa_rope_table (or the caller's own), of table_rows rows: N
+ *   (every batch entry has the same positions; row n) or B * N (row b N + n).
+ *   Arithmetic: fp32, each product and each sum rounded once (no FMA), then
+ *   one rounding to dtype.
+ */
+LLSA_API int llsa_rope(const llsa_rope_desc* rope, int B, int H, int N, int D, int dtype, const float* table,
+                       int table_rows, const void* q, const void* k, void* q_out, void* k_out, int adjoint,
+                       void* stream);
+
+/*
+ * llsa_rope_pool - llsa_rope of Q and K and llsa_pool of the rotated Q, K and
+ * of V in one pass: the rotated values are summed while they are still in
+ * registers.  Writes exactly what the two calls write, bit for bit.
+ *   desc, out: as llsa_pool takes them.  table, table_rows, q, k, q_out,
+ *   k_out: as llsa_rope takes them (all required; q_out may be q, k_out may be
+ *   k).  v: [B, H, N, D], read.
+ */
+LLSA_API int llsa_rope_pool(const llsa_desc* desc, const llsa_rope_desc* rope, const float* table, int table_rows,
+                            const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                            const llsa_pyramid* out, void* stream);
+
+/* -------------------------------------------------------- cross attention
+ *
+ * Attention of N query tokens to the S states of an encoder (a caption, a
+ * low-resolution image): the other attention of a conditioned diffusion
+ * transformer's block, dense and of two lengths.
+ */
+
+/* Problem description (plain data, passed by pointer, read before launch). */
+typedef struct {
+  int B;          /* batch entries, >= 1 */
+  int H;          /* query heads, >= 1 */
+  int Hkv;        /* key heads, >= 1, dividing H: query head h reads key head h / (H / Hkv) */
+  int N;          /* query tokens, >= 1, any length and order */
+  int S;          /* encoder states, >= 0 */
+  int D;          /* head dim, 64 or 128 */
+  int dtype;      /* LLSA_F32 or LLSA_BF16 */
+  int flags;      /* must be 0 */
+  float sm_scale; /* softmax scale; 0 selects 1/sqrt(D) */
+} llsa_cross_desc;
+
+/* Device scratch sizes of the two calls below for desc; 0 on an invalid desc
+ * and where the call needs none. */
+LLSA_API size_t llsa_cross_fwd_workspace_bytes(const llsa_cross_desc* desc);
+LLSA_API size_t llsa_cross_bwd_workspace_bytes(const llsa_cross_desc* desc);
+
+/*
+ * llsa_cross_attn_fwd - cross attention.
+ *     s_ij  = sm_scale * q_i . k_j            over the keys j that b may see
+ *     O_i   = sum_j e^{s_ij} v_j / sum_j e^{s_ij}
+ *     lse_i = ln sum_j e^{s_ij}
+ *   A query without keys gets O_i = 0 and lse_i = -inf.
+ *   q: [B, H, N, D]; k, v: [B, Hkv, S, D]; o: [B, H, N, D], written; all of
+ *   dtype, 16-byte aligned.  k and v may be NULL when S = 0.
+ *   kv_len: int32 [B] or NULL.  Batch entry b sees states 0 .. kv_len[b] - 1
+ *   (values outside [0, S] count as the nearer end); NULL: all S.
+ *   key_mask: uint8 [B, S] or NULL.  A state with a zero is not seen.  What k
+ *   and v hold at states that are not seen is of no effect, NaN included.
+ *   o_res: [B, H, N, D] bf16 or NULL; the bf16 rounding residual of O, as
+ *   llsa_attn_fwd_res writes it, for a more exact backward (dtype LLSA_F32:
+ *   not used).
+ *   lse: fp32 [B, H, N], written.
+ *   ws: device scratch of ws_bytes >= llsa_cross_fwd_workspace_bytes(desc),
+ *   256-byte aligned (may be NULL when that is 0); not read before it is
+ *   written.  dev_status: may be NULL; LLSA_DEV_TIMEOUT if a bounded wait of
+ *   the kernel gave up.
+ *   Outputs and ws overlap nothing (else LLSA_ERR_INVALID_ARG).  Sums run in a
+ *   fixed order: results are identical from run to run.
+ */
+LLSA_API int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, const void* k, const void* v,
+                                 const int32_t* kv_len, const uint8_t* key_mask, void* o, void* o_res, float* lse,
+                                 void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * llsa_cross_attn_bwd - gradients of llsa_cross_attn_fwd.
+ *   With P_ij = e^{s_ij - lse_i} and Delta_i = dO_i . O_i:
+ *     dS_ij = P_ij (dO_i . v_j - Delta_i)
+ *     dQ_i  = sm_scale * sum_j dS_ij k_j
+ *     dk_j  = sm_scale * sum_i dS_ij q_i ,  dv_j = sum_i P_ij dO_i
+ *   with the sums over i running over every query head that reads the key
+ *   head.  States that are not seen get zero gradients.
+ *   o, lse: the forward's outputs.  o_res: the forward's residual or NULL;
+ *   with it Delta_i = dO_i . (o_i + o_res_i).  dout: dO.  dq: [B, H, N, D],
+ *   dk, dv: [B, Hkv, S, D], of dtype, written (dk, dv may be NULL when S = 0).
+ *   All 16-byte aligned.  kv_len, key_mask: as the forward took them.
+ *   ws: device scratch of ws_bytes >= llsa_cross_bwd_workspace_bytes(desc),
+ *   256-byte aligned (may be NULL when that is 0); not read before it is
+ *   written.  dev_status: may be NULL.
+ *   Outputs and ws overlap nothing (else LLSA_ERR_INVALID_ARG).  Sums run in a
+ *   fixed order without global atomics: results are identical from run to run.
+ */
+LLSA_API int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* k, const void* v,
+                                 const int32_t* kv_len, const uint8_t* key_mask, const void* o, const void* o_res,
+                                 const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
+                                 size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /*
  * llsa_selftest_wait_timeout - a check of the kernels' bounded waits.
  *   The paper has no counterpart: this is a test hook of this library.  The
