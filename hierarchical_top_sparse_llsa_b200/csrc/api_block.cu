@@ -145,9 +145,14 @@ inline size_t take(size_t* off, size_t bytes) {
   return at;
 }
 
+// Query rows of a key head.
+inline int rows_per_key_head(const llsa_cross_desc* d) { return d->H / d->Hkv * d->N; }
+
 CrossWs cross_fwd_ws(const llsa_cross_desc* d) {
   CrossWs w;
-  w.plan = cross_simt_fwd_plan(d);
+  const long long BH = (long long)d->B * d->Hkv;
+  w.plan = d->dtype == LLSA_BF16 ? cross_tc_fwd_plan(BH, rows_per_key_head(d), d->S)
+                                 : cross_simt_fwd_plan(BH, rows_per_key_head(d), d->S);
   const size_t rows = (size_t)d->B * d->H * d->N;
   if (w.plan.nks > 1) {
     w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
@@ -158,7 +163,7 @@ CrossWs cross_fwd_ws(const llsa_cross_desc* d) {
 
 CrossWs cross_bwd_ws(const llsa_cross_desc* d) {
   CrossWs w;
-  w.plan = cross_simt_bwd_plan(d);
+  w.plan = cross_simt_bwd_plan((long long)d->B * d->Hkv, rows_per_key_head(d), d->S);
   const size_t rows = (size_t)d->B * d->H * d->N, keys = (size_t)d->B * d->Hkv * d->S;
   w.delta = take(&w.total, rows * sizeof(float));
   if (w.plan.nks > 1) w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
@@ -167,6 +172,35 @@ CrossWs cross_bwd_ws(const llsa_cross_desc* d) {
     w.c = take(&w.total, w.plan.nz * keys * d->D * sizeof(float));
   }
   return w;
+}
+
+// A bf16 [heads, rows, D] tensor seen by TMA as boxes of 128 rows x 64
+// columns (128 bytes) of one head with 128-byte swizzle; rows past a head's
+// last read as zeros and are not written.
+int make_head_map(CUtensorMap* map, const void* ptr, long long heads, int rows, int D) {
+  EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return LLSA_ERR_LAUNCH;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
+  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estride,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LLSA_OK : LLSA_ERR_LAUNCH;
+}
+
+// Maps of tensors[i], i < n, each of the queries' rows or (kv[i]) the keys'.
+// Without keys the latter are never read: the queries' map stands in.
+int make_cross_maps(CUtensorMap* maps, const llsa_cross_desc* d, const void* const* tensors, const bool* kv, int n) {
+  const long long heads = (long long)d->B * d->Hkv;
+  for (int i = 0; i < n; ++i) {
+    const bool keys = kv[i] && d->S > 0;
+    const int st = make_head_map(&maps[i], kv[i] && !keys ? tensors[0] : tensors[i], heads,
+                                 keys ? d->S : rows_per_key_head(d), d->D);
+    if (st != LLSA_OK) return st;
+  }
+  return LLSA_OK;
 }
 
 int check_ws(const void* ws, size_t ws_bytes, size_t need) {
@@ -186,9 +220,8 @@ CrossParams cross_params(const llsa_cross_desc* d, const void* q, const void* k,
   p.mask = mask;
   p.status = status;
   p.B = d->B;
-  p.H = d->H;
-  p.Hkv = d->Hkv;
-  p.N = d->N;
+  p.H = d->Hkv;
+  p.N = rows_per_key_head(d);
   p.S = d->S;
   p.D = d->D;
   p.nks = plan.nks;
@@ -324,7 +357,17 @@ int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, const void* 
     p.part_ml = reinterpret_cast<float2*>(base + w.b);
   }
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t err = launch_cross_fwd_simt(p, desc->dtype, s);
+  cudaError_t err;
+  if (desc->dtype == LLSA_BF16) {
+    CUtensorMap maps[4];
+    const void* const tensors[4] = {q, k, v, o};
+    const bool kv[4] = {false, true, true, false};
+    st = make_cross_maps(maps, desc, tensors, kv, 4);
+    if (st != LLSA_OK) return st;
+    err = launch_cross_fwd_tc(p, maps, s);
+  } else {
+    err = launch_cross_fwd_simt(p, desc->dtype, s);
+  }
   if (err == cudaSuccess && p.nks > 1) err = launch_cross_combine(p, desc->dtype, s);
   return launch_status(err);
 }

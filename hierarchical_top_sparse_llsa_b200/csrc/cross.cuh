@@ -1,6 +1,8 @@
 // Launch parameters of the cross-attention kernels (not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
+
 #include "llsa_internal.cuh"
 
 namespace llsa {
@@ -25,10 +27,14 @@ struct CrossParams {
   float2* part_ml; // fwd, nks > 1: [nks][B H N], their maxima (base 2) and sums
   float* delta;    // bwd: [B H N]
   float* part_dq;  // bwd, nks > 1: [nks][B H N][D]
-  float* part_dk;  // bwd, nz > 1: [nz][B Hkv S][D]
+  float* part_dk;  // bwd, nz > 1: [nz][B H S][D]
   float* part_dv;
   int32_t* status;
-  int B, H, Hkv, N, S, D;
+  // The query heads of a key head are neighbours in memory and see the same
+  // keys: the kernels take them as one run of rows.
+  int B, H;        // batch entries, key heads
+  int N;           // query rows of a key head: (query heads / key heads) x query tokens
+  int S, D;
   int nks;         // splits of the keys (fwd: of O; bwd: of dQ)
   int nz;          // bwd: segments of the query tiles (dK, dV)
   float scale;
@@ -45,9 +51,14 @@ __device__ __forceinline__ int cross_len(const CrossParams& p, int b) {
 struct CrossPlan {
   int nks, nz;
 };
-CrossPlan cross_simt_fwd_plan(const llsa_cross_desc* d);
-CrossPlan cross_simt_bwd_plan(const llsa_cross_desc* d);
+CrossPlan cross_simt_fwd_plan(long long BH, int N, int S);
+CrossPlan cross_simt_bwd_plan(long long BH, int N, int S);
+CrossPlan cross_tc_fwd_plan(long long BH, int N, int S);
 
+constexpr int kCrossSms = 148;  // SMs of a B200
+
+// maps: Q, K, V, O as 3D [B H, rows, D] bf16, box 128 rows x 64 columns, 128-byte swizzle
+cudaError_t launch_cross_fwd_tc(const CrossParams& p, const CUtensorMap* maps, cudaStream_t s);
 cudaError_t launch_cross_fwd_simt(const CrossParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_cross_bwd_simt(const CrossParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_cross_combine(const CrossParams& p, int dtype, cudaStream_t s);

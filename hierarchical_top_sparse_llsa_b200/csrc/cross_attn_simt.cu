@@ -27,9 +27,8 @@ constexpr int kFwdThreads = 128;
 constexpr int kBwdThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kSms = 148;
 
-inline int tiles_of(int n) { return (n + kT - 1) / kT; }
+inline int tiles_of(int n) { return n / kT + (n % kT != 0); }
 
 // rows r < nrows of src [.., D] (kept where keep is null or keep[r] != 0) as
 // floats into dst rows of LD floats; the others as zeros
@@ -113,8 +112,8 @@ cross_fwd_simt(CrossParams p, int qtiles) {
   id /= qtiles;
   const int split = (int)(id % p.nks);
   const int bh = (int)(id / p.nks);
-  const int b = bh / p.H, h = bh % p.H;
-  const size_t kvrow = ((size_t)b * p.Hkv + h / (p.H / p.Hkv)) * p.S;
+  const int b = bh / p.H;
+  const size_t kvrow = (size_t)bh * p.S;
   const int q0 = qt * kT, nq = min(kT, p.N - q0);
   const size_t row0 = (size_t)bh * p.N + q0;
   const int len = cross_len(p, b);
@@ -240,7 +239,8 @@ cross_combine_kernel(CrossParams p) {
 #pragma unroll 4
   for (int z = 0; z < p.nks; ++z) {
     const float2 ml = p.part_ml[z * rows + row];
-    const float w = exp2f(ml.x - mb);  // 0 for a split without keys
+    if (ml.x == -INFINITY) continue;  // a split without keys: its O may not be written
+    const float w = exp2f(ml.x - mb);
     l = fmaf(ml.y, w, l);
     const float* src = p.part_o + (z * rows + row) * D + lane * C;
     if (C == 2) {
@@ -349,8 +349,8 @@ cross_dq_simt(CrossParams p, int qtiles) {
   id /= qtiles;
   const int split = (int)(id % p.nks);
   const int bh = (int)(id / p.nks);
-  const int b = bh / p.H, h = bh % p.H;
-  const size_t kvrow = ((size_t)b * p.Hkv + h / (p.H / p.Hkv)) * p.S;
+  const int b = bh / p.H;
+  const size_t kvrow = (size_t)bh * p.S;
   const int q0 = qt * kT, nq = min(kT, p.N - q0);
   const size_t row0 = (size_t)bh * p.N + q0;
   const int len = cross_len(p, b);
@@ -410,8 +410,7 @@ cross_dq_simt(CrossParams p, int qtiles) {
   }
 }
 
-// dK and dV of one key tile over one segment of the query tiles of the heads
-// that read its key head.
+// dK and dV of one key tile over one segment of the query tiles.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads)
 cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
@@ -425,11 +424,10 @@ cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
   const int kt = (int)(id % ktiles);
   id /= ktiles;
   const int z = (int)(id % p.nz);
-  const int bk = (int)(id / p.nz);  // b * Hkv + key head
-  const int b = bk / p.Hkv, hk = bk % p.Hkv;
-  const int group = p.H / p.Hkv;
+  const int bh = (int)(id / p.nz);
+  const int b = bh / p.H;
   const int k0 = kt * kT, nk = min(kT, p.S - k0);
-  const size_t kvrow = (size_t)bk * p.S + k0;
+  const size_t kvrow = (size_t)bh * p.S + k0;
   const int len = cross_len(p, b);
   load_keep(keep, p, b, k0, len);
   __syncthreads();
@@ -440,13 +438,11 @@ cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
-  const long long items = (long long)group * qtiles;
-  long long it = items * z / p.nz;
-  const long long it1 = k0 < len ? items * (z + 1) / p.nz : it;  // a tile past the end gets zeros
-  for (; it < it1; ++it) {
-    const int h = hk * group + (int)(it / qtiles), qt = (int)(it % qtiles);
+  int qt = (int)((long long)qtiles * z / p.nz);
+  const int qt1 = k0 < len ? (int)((long long)qtiles * (z + 1) / p.nz) : qt;  // a tile past the end gets zeros
+  for (; qt < qt1; ++qt) {
     const int q0 = qt * kT, nq = min(kT, p.N - q0);
-    const size_t row0 = ((size_t)b * p.H + h) * p.N + q0;
+    const size_t row0 = (size_t)bh * p.N + q0;
     __syncthreads();
     load_rows<T, D, LD, kBwdThreads>(Q, static_cast<const T*>(p.q) + row0 * D, nq, nullptr);
     load_rows<T, D, LD, kBwdThreads>(dO, static_cast<const T*>(p.dout) + row0 * D, nq, nullptr);
@@ -484,7 +480,7 @@ cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
     for (int c = 0; c < D / 64; ++c) {
       const size_t at = (kvrow + r) * D + c * 64 + tx * 4;
       if (p.nz > 1) {
-        const size_t off = (size_t)z * p.B * p.Hkv * p.S * D + at;
+        const size_t off = (size_t)z * p.B * p.H * p.S * D + at;
         store4(p.part_dk + off, &ak[i][4 * c]);
         store4(p.part_dv + off, &av[i][4 * c]);
       } else {
@@ -536,7 +532,7 @@ cudaError_t fwd_typed(const CrossParams& p, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t bwd_typed(const CrossParams& p, cudaStream_t s) {
   const int qt = tiles_of(p.N), kt = tiles_of(p.S);
-  const long long b1 = (long long)p.B * p.H * p.nks * qt, b2 = (long long)p.B * p.Hkv * p.nz * kt;
+  const long long b1 = (long long)p.B * p.H * p.nks * qt, b2 = (long long)p.B * p.H * p.nz * kt;
   if (b1 > 0x7fffffffLL || b2 > 0x7fffffffLL) return cudaErrorInvalidValue;
   const size_t smem = BwdSmem<D>::kFloats * sizeof(float);
   cudaError_t e = allow_smem(cross_dq_simt<T, D>, smem);
@@ -566,24 +562,17 @@ cudaError_t rows_dispatch(const CrossParams& p, int dtype, bool combine, cudaStr
 // parts of n tiles so that units * parts reaches about two blocks per SM
 int parts_for(long long units, int n) {
   if (n < 1) return 1;
-  long long parts = (2LL * kSms + units - 1) / units;
+  long long parts = (2LL * kCrossSms + units - 1) / units;
   if (parts > n) parts = n;
   return parts < 1 ? 1 : (int)parts;
 }
 
 }  // namespace
 
-CrossPlan cross_simt_fwd_plan(const llsa_cross_desc* d) {
-  return {parts_for((long long)d->B * d->H * tiles_of(d->N), tiles_of(d->S)), 1};
-}
+CrossPlan cross_simt_fwd_plan(long long BH, int N, int S) { return {parts_for(BH * tiles_of(N), tiles_of(S)), 1}; }
 
-CrossPlan cross_simt_bwd_plan(const llsa_cross_desc* d) {
-  CrossPlan c;
-  c.nks = parts_for((long long)d->B * d->H * tiles_of(d->N), tiles_of(d->S));
-  const long long kunits = (long long)d->B * d->Hkv * (d->S > 0 ? tiles_of(d->S) : 1);
-  const long long items = (long long)(d->H / d->Hkv) * tiles_of(d->N);
-  c.nz = parts_for(kunits, items > 0x7fffffff ? 0x7fffffff : (int)items);
-  return c;
+CrossPlan cross_simt_bwd_plan(long long BH, int N, int S) {
+  return {parts_for(BH * tiles_of(N), tiles_of(S)), parts_for(BH * (S > 0 ? tiles_of(S) : 1), tiles_of(N))};
 }
 
 cudaError_t launch_cross_fwd_simt(const CrossParams& p, int dtype, cudaStream_t s) {
