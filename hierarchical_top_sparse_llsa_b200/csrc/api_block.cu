@@ -136,7 +136,8 @@ int check_cross(const llsa_cross_desc* d) {
 
 struct CrossWs {
   CrossPlan plan;
-  size_t delta = 0, a = 0, b = 0, c = 0, total = 0;  // a: O or dQ parts, b: (m, l) or dK parts, c: dV parts
+  // a: O or dQ parts, a2, s: more of dQ's, b: (m, l) or dK parts, c: dV parts
+  size_t delta = 0, alone = 0, a = 0, a2 = 0, s = 0, b = 0, c = 0, total = 0;
 };
 
 inline size_t take(size_t* off, size_t bytes) {
@@ -163,10 +164,21 @@ CrossWs cross_fwd_ws(const llsa_cross_desc* d) {
 
 CrossWs cross_bwd_ws(const llsa_cross_desc* d) {
   CrossWs w;
-  w.plan = cross_simt_bwd_plan((long long)d->B * d->Hkv, rows_per_key_head(d), d->S);
-  const size_t rows = (size_t)d->B * d->H * d->N, keys = (size_t)d->B * d->Hkv * d->S;
+  const bool tc = d->dtype == LLSA_BF16;
+  const long long BH = (long long)d->B * d->Hkv;
+  w.plan = (tc ? cross_tc_bwd_plan : cross_simt_bwd_plan)(BH, rows_per_key_head(d), d->S);
+  const size_t rows = (size_t)d->B * d->H * d->N;
+  // keys, in whole tiles where the parts are
+  const size_t keys = (size_t)BH * (tc ? ((size_t)d->S + 127) / 128 * 128 : (size_t)d->S);
   w.delta = take(&w.total, rows * sizeof(float));
-  if (w.plan.nks > 1) w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
+  w.alone = take(&w.total, (size_t)d->B * sizeof(int32_t));
+  if (w.plan.nks > 1) {
+    w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
+    if (tc) {
+      w.a2 = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
+      w.s = take(&w.total, w.plan.nks * rows * sizeof(float4));
+    }
+  }
   if (w.plan.nz > 1) {
     w.b = take(&w.total, w.plan.nz * keys * d->D * sizeof(float));
     w.c = take(&w.total, w.plan.nz * keys * d->D * sizeof(float));
@@ -174,15 +186,15 @@ CrossWs cross_bwd_ws(const llsa_cross_desc* d) {
   return w;
 }
 
-// A bf16 [heads, rows, D] tensor seen by TMA as boxes of 128 rows x 64
-// columns (128 bytes) of one head with 128-byte swizzle; rows past a head's
+// A bf16 [heads, rows, D] tensor seen by TMA as boxes of `box_rows` rows
+// x 64 columns (128 bytes) of one head with 128-byte swizzle; rows past a head's
 // last read as zeros and are not written.
-int make_head_map(CUtensorMap* map, const void* ptr, long long heads, int rows, int D) {
+int make_head_map(CUtensorMap* map, const void* ptr, long long heads, int rows, int D, int box_rows) {
   EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return LLSA_ERR_LAUNCH;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
-  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   const cuuint32_t estride[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estride,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -190,14 +202,21 @@ int make_head_map(CUtensorMap* map, const void* ptr, long long heads, int rows, 
   return r == CUDA_SUCCESS ? LLSA_OK : LLSA_ERR_LAUNCH;
 }
 
-// Maps of tensors[i], i < n, each of the queries' rows or (kv[i]) the keys'.
-// Without keys the latter are never read: the queries' map stands in.
-int make_cross_maps(CUtensorMap* maps, const llsa_cross_desc* d, const void* const* tensors, const bool* kv, int n) {
-  const long long heads = (long long)d->B * d->Hkv;
+// Maps of n tensors of the queries' rows.
+int make_query_maps(CUtensorMap* maps, const llsa_cross_desc* d, const void* const* tensors, int n, int box_rows) {
   for (int i = 0; i < n; ++i) {
-    const bool keys = kv[i] && d->S > 0;
-    const int st = make_head_map(&maps[i], kv[i] && !keys ? tensors[0] : tensors[i], heads,
-                                 keys ? d->S : rows_per_key_head(d), d->D);
+    const int st = make_head_map(&maps[i], tensors[i], (long long)d->B * d->Hkv, rows_per_key_head(d), d->D, box_rows);
+    if (st != LLSA_OK) return st;
+  }
+  return LLSA_OK;
+}
+
+// Maps of K and V.  Without keys they are never read: q stands in.
+int make_key_maps(CUtensorMap* maps, const llsa_cross_desc* d, const void* k, const void* v, const void* q,
+                  int box_rows) {
+  const void* const tensors[2] = {d->S > 0 ? k : q, d->S > 0 ? v : q};
+  for (int i = 0; i < 2; ++i) {
+    const int st = make_head_map(&maps[i], tensors[i], (long long)d->B * d->Hkv, d->S > 0 ? d->S : 1, d->D, box_rows);
     if (st != LLSA_OK) return st;
   }
   return LLSA_OK;
@@ -359,11 +378,12 @@ int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, const void* 
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t err;
   if (desc->dtype == LLSA_BF16) {
-    CUtensorMap maps[4];
-    const void* const tensors[4] = {q, k, v, o};
-    const bool kv[4] = {false, true, true, false};
-    st = make_cross_maps(maps, desc, tensors, kv, 4);
+    CUtensorMap qo[2], kv[2];
+    const void* const rows_of[2] = {q, o};
+    st = make_query_maps(qo, desc, rows_of, 2, 128);
+    if (st == LLSA_OK) st = make_key_maps(kv, desc, k, v, q, 128);
     if (st != LLSA_OK) return st;
+    const CUtensorMap maps[4] = {qo[0], kv[0], kv[1], qo[1]};
     err = launch_cross_fwd_tc(p, maps, s);
   } else {
     err = launch_cross_fwd_simt(p, desc->dtype, s);
@@ -403,12 +423,27 @@ int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* 
   p.dv = dv;
   char* base = static_cast<char*>(ws);
   p.delta = reinterpret_cast<float*>(base + w.delta);
-  if (p.nks > 1) p.part_dq = reinterpret_cast<float*>(base + w.a);
+  p.alone = reinterpret_cast<int32_t*>(base + w.alone);
+  if (p.nks > 1) {
+    p.part_dq = reinterpret_cast<float*>(base + w.a);
+    p.part_dqb = reinterpret_cast<float*>(base + w.a2);
+    p.part_s = reinterpret_cast<float4*>(base + w.s);
+  }
   if (p.nz > 1) {
     p.part_dk = reinterpret_cast<float*>(base + w.b);
     p.part_dv = reinterpret_cast<float*>(base + w.c);
   }
   const cudaStream_t s = (cudaStream_t)stream;
+  if (desc->dtype == LLSA_BF16) {
+    CUtensorMap q128[2], q64[2], kv128[2], kv64[2];
+    const void* const rows_of[2] = {q, dout};
+    st = make_query_maps(q128, desc, rows_of, 2, 128);
+    if (st == LLSA_OK) st = make_query_maps(q64, desc, rows_of, 2, 64);
+    if (st == LLSA_OK) st = make_key_maps(kv128, desc, k, v, q, 128);
+    if (st == LLSA_OK) st = make_key_maps(kv64, desc, k, v, q, 64);
+    if (st != LLSA_OK) return st;
+    return launch_status(launch_cross_bwd_tc(p, q128, kv64, kv128, q64, s));
+  }
   cudaError_t e = launch_cross_delta(p, desc->dtype, s);
   if (e == cudaSuccess) e = launch_cross_bwd_simt(p, desc->dtype, s);
   if (e == cudaSuccess && p.nks > 1)

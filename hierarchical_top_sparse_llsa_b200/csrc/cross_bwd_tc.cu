@@ -1,0 +1,719 @@
+// Cross attention backward on the 5th-generation tensor cores (tcgen05), bf16,
+// D = 64 or 128:
+//   P = e^(scale S - lse),  S = Q K^T,      dP = dO V^T
+//   Delta_i = sum_j P_ij dP_ij,             dS = P (dP - Delta)
+//   dQ = scale dS K,  dK = scale dS^T Q,    dV = P^T dO
+// in two passes of one kernel: the first (kDq) walks the keys for 128 queries
+// and gives dQ and Delta, the second walks the queries for 128 keys and gives
+// dK and dV.  Both have the same shape.  With A1, A2 the 128 rows that stay
+// (Q, dO; K, V) and N1, N2 the 64 rows that stream by (K, V; Q, dO):
+//   S = A1 N1^T, dP = A2 N2^T     into tensor memory,
+//   P and dS                      bf16, over them in tensor memory,
+//   accA += dS N1, accB += P N1 (first pass) or P N2 (second pass),
+// so neither P nor dS goes through shared memory.  Two stages of S and dP
+// alternate between two groups of four warps, one thread per row: the tensor
+// cores fill one while the exponentials of the other are computed.
+//
+// Delta is formed from unrounded terms and in the same walk as dQ.  With any
+// number c per row, dS = P (dP - c) + P (c - Delta), so
+//   dQ = scale (sum_j P (dP - c) K + (c - Delta) sum_j P K),
+//   Delta = c sum_j P + sum_j P (dP - c);
+// c, the mean of dP over the first 32 keys weighted with P, is near Delta, so
+// the rounding of P (dP - c) to bf16 is that of dS, and all of it is exact in
+// c.  (Delta from the stored O would carry O's rounding to bf16, which the
+// keys' common part lifts above the gradient where many keys share a row.)
+// A query that sees one key alone has dS = 0: P is 1 whatever the score.
+//
+//   warps 0-3, 4-7  the two groups, also the epilogue;
+//   warp 8          TMA loads of A (two buffers) and N (a ring);
+//   warp 9          one thread issues the MMAs;
+//   warp 10         first pass: with lengths or a mask, the bits of the keys
+//                   seen and zeros over the K rows that are not (their dS is
+//                   zero, and zero times NaN is NaN); second pass: lse and
+//                   Delta of the queries that stream by.
+// The second pass cuts all its (key tile, query tile) pairs into equal runs,
+// one per SM; a key tile that several SMs share is summed by a last kernel, in
+// a fixed order.  The first pass cuts the keys where there are few rows.
+// Every wait is bounded; a time-out is reported as LLSA_DEV_TIMEOUT.
+
+#include <math.h>
+
+#include "cross.cuh"
+#include "cross_tc.cuh"
+
+namespace llsa {
+
+namespace {
+
+constexpr int kThreads = 352;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpAux = 10;
+
+template <int D>
+struct Cfg {
+  static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
+  static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
+  static constexpr int kSlots = (D == 64) ? 6 : 3;
+  static constexpr int kOffN = 4 * kA;     // two buffers of A1, A2
+  static constexpr int kEnd = kOffN + kSlots * 2 * kN;
+  static constexpr uint32_t kColAcc = 256;  // S_0 dP_0 | S_1 dP_1 | accA | accB
+};
+
+template <int NS>
+struct Shared {
+  uint64_t a_full[2], a_empty[2], n_full[NS], n_empty[NS], n_aux[NS];
+  uint64_t s_full[2], p_full[2], acc_full, acc_free, c_full, x_full, x_read, done;
+  uint32_t tmem_base;
+  uint32_t bits[NS][2];  // first pass: keys seen, by slot
+  union alignas(16) {
+    struct {
+      float c[128];          // of the item's rows
+      float2 sums[2][128];   // each group's sum P, sum P (dP - c)
+    } q;
+    float2 side[NS][64];     // second pass, by slot: [0..31] -lse of 64 queries, [32..63] their Delta
+  };
+};
+
+// The items of a CTA, in order.  First pass: 128 query rows against one range
+// of the keys.  Second pass: 128 keys against one range of the queries, cut
+// from the CTA's share of all pairs.
+template <bool kDq>
+struct BwdItems {
+  const CrossParams& p;
+  CrossPairs w;                // second pass
+  int i, end, nt;              // kDq: items; else units (key tiles); nt: row tiles per head
+  long long beg, fin;          // second pass: the CTA's pairs
+  int bk, b, split, slot, r0, len;
+  int n0, n;                   // first tile of 64 streamed rows, how many
+  bool new_b;
+
+  __device__ __forceinline__ BwdItems(const CrossParams& p_)
+      : p(p_), w((long long)p_.B * p_.H, p_.N, p_.S, p_.nz, (int)gridDim.x), b(-1) {
+    if (kDq) {
+      nt = (p.N + 127) / 128;
+      const long long items = (long long)p.B * p.H * p.nks * nt;
+      i = (int)(items * blockIdx.x / gridDim.x) - 1;
+      end = (int)(items * (blockIdx.x + 1) / gridDim.x);
+    } else {
+      nt = (p.S + 127) / 128;
+      beg = w.begin(blockIdx.x);
+      fin = w.begin(blockIdx.x + 1);
+      i = (int)(beg / w.nq) - 1;
+      end = (int)((fin + w.nq - 1) / w.nq);
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (++i >= end) return false;
+    const int run = i / nt;
+    r0 = (i - run * nt) * 128;
+    bk = kDq ? run / p.nks : run;
+    const int nb = bk / p.H;
+    new_b = nb != b;
+    if (new_b) {
+      b = nb;
+      len = cross_len(p, b);
+    }
+    if (kDq) {
+      split = run - bk * p.nks;
+      const int kt = (len + 63) / 64;
+      n0 = (int)((long long)kt * split / p.nks);
+      n = (int)((long long)kt * (split + 1) / p.nks) - n0;
+    } else {
+      const long long u = (long long)i * w.nq;
+      n0 = (int)(beg > u ? beg - u : 0);
+      n = (int)(fin < u + w.nq ? fin - u : w.nq) - n0;
+      slot = p.nz > 1 ? (int)blockIdx.x - w.cta_of(u) : 0;
+      if (r0 >= len) n = 0;  // no key of the tile is seen
+    }
+    return true;
+  }
+  // 16-row steps of the item's tile j
+  __device__ __forceinline__ int steps(int j) const {
+    if (!kDq) return 4;
+    const int m = len - (n0 + j) * 64;
+    return m >= 64 ? 4 : (m + 15) >> 4;
+  }
+};
+
+// -lse in units of log2; without keys (lse = -inf) every probability is zero.
+__device__ __forceinline__ float neg_lse2(float lse) { return lse == -INFINITY ? lse : -lse * kLog2e; }
+
+// Whether b sees at most one key (a whole warp asks).
+__device__ __forceinline__ bool sees_one(const CrossParams& p, int b, int len) {
+  if (p.mask == nullptr || len <= 1) return len <= 1;
+  const uint8_t* m = p.mask + (size_t)b * p.S;
+  const int lane = threadIdx.x & 31;
+  int seen = 0;
+  for (int k0 = 0; k0 < len && seen < 2; k0 += 256) {
+    bool on[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + 32 * u + lane;
+      on[u] = k < len && m[k] != 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) seen += __popc(__ballot_sync(0xffffffffu, on[u]));
+  }
+  return seen <= 1;
+}
+
+template <int D, bool kDq>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap ta2,
+                    const __grid_constant__ CUtensorMap tn1, const __grid_constant__ CUtensorMap tn2, CrossParams p) {
+  using C = Cfg<D>;
+  constexpr int H = D / 64;  // 64-column halves of a tile
+  constexpr int NS = C::kSlots;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  using Sh = Shared<NS>;
+  Sh& S = *reinterpret_cast<Sh*>(sm + C::kEnd);
+  const uint32_t base = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool clean = kDq && (p.mask != nullptr || p.kv_len != nullptr);
+  bool ok = true;
+
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(&S.tmem_base), 512);
+    tmem_relinquish();
+  } else if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&S.a_full[i]), 1);
+      mbar_init(smem_u32(&S.a_empty[i]), 1);
+      mbar_init(smem_u32(&S.s_full[i]), 1);
+      mbar_init(smem_u32(&S.p_full[i]), 128);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&S.n_full[i]), 1);
+      mbar_init(smem_u32(&S.n_empty[i]), 1);
+      mbar_init(smem_u32(&S.n_aux[i]), 1);
+    }
+    mbar_init(smem_u32(&S.acc_full), 1);
+    mbar_init(smem_u32(&S.acc_free), 256);
+    mbar_init(smem_u32(&S.c_full), 128);
+    mbar_init(smem_u32(&S.x_full), 256);
+    mbar_init(smem_u32(&S.x_read), 256);
+    mbar_init(smem_u32(&S.done), 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = S.tmem_base;
+  auto abuf = [&](int a) { return base + (uint32_t)(a & 1) * 2 * C::kA; };
+  auto nslot = [&](int s) { return base + C::kOffN + (uint32_t)(s % NS) * 2 * C::kN; };
+  BwdItems<kDq> it(p);
+
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      int a = 0, s = 0;  // items and streamed tiles so far
+      for (; ok && it.next();) {
+        if (it.n == 0) continue;
+        uint64_t* full = &S.a_full[a & 1];
+        if (a >= 2) ok = mbar_wait_bounded(smem_u32(&S.a_empty[a & 1]), (uint32_t)((a / 2 - 1) & 1));
+        if (!ok) break;
+        mbar_arrive_expect_tx(smem_u32(full), 2 * C::kA);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          tma_load_3d(abuf(a) + h * 16384, &ta1, 64 * h, it.r0, it.bk, smem_u32(full));
+          tma_load_3d(abuf(a) + C::kA + h * 16384, &ta2, 64 * h, it.r0, it.bk, smem_u32(full));
+        }
+        ++a;
+        for (int j = 0; j < it.n; ++j, ++s) {
+          if (s >= NS) ok = mbar_wait_bounded(smem_u32(&S.n_empty[s % NS]), (uint32_t)((s / NS - 1) & 1));
+          if (!ok) break;
+          full = &S.n_full[s % NS];
+          mbar_arrive_expect_tx(smem_u32(full), 2 * C::kN);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            tma_load_3d(nslot(s) + h * 8192, &tn1, 64 * h, (it.n0 + j) * 64, it.bk, smem_u32(full));
+            tma_load_3d(nslot(s) + C::kN + h * 8192, &tn2, 64 * h, (it.n0 + j) * 64, it.bk, smem_u32(full));
+          }
+        }
+      }
+      // no copy may still be landing when the CTA exits
+      for (int i = a > 2 ? a - 2 : 0; i < a; ++i)
+        if (!mbar_wait_bounded(smem_u32(&S.a_full[i & 1]), (uint32_t)((i / 2) & 1))) ok = false;
+      for (int i = s > NS ? s - NS : 0; i < s; ++i)
+        if (!mbar_wait_bounded(smem_u32(&S.n_full[i % NS]), (uint32_t)((i / NS) & 1))) ok = false;
+    }
+  } else if (warp == kWarpMma) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1, 0);
+      constexpr uint32_t kSecond = kDq ? 0 : C::kN;  // accB's right side: N1 or N2
+      int a = 0, s = 0;
+      bool pend = false, pfirst = false, plast = false;
+      int ps = 0, pa = 0, pnt = 0;   // the pending products' tile, item and 16-row steps
+      auto products = [&]() {        // accA (+)= dS N1, accB (+)= P N1 or N2
+        if (!pend) return;
+        pend = false;
+        const int g = ps & 1;
+        if (kDq && clean) ok = mbar_wait_bounded(smem_u32(&S.n_aux[ps % NS]), (uint32_t)((ps / NS) & 1));
+        if (ok) ok = mbar_wait_bounded(smem_u32(&S.p_full[g]), (uint32_t)((ps >> 1) & 1));
+        if (ok && pfirst && pa > 0) ok = mbar_wait_bounded(smem_u32(&S.acc_free), (uint32_t)((pa - 1) & 1));
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t ts = tbase + (uint32_t)g * 128;
+        for (int k = 0; k < pnt; ++k)
+          tc_mma_f16_ts(tbase + C::kColAcc + D, ts + (uint32_t)k * 8,
+                        smem_desc_sw128(nslot(ps) + kSecond + (uint32_t)k * 2048, 8192, 1024), idesc_acc,
+                        (!pfirst || k > 0));
+        for (int k = 0; k < pnt; ++k)
+          tc_mma_f16_ts(tbase + C::kColAcc, ts + 64 + (uint32_t)k * 8,
+                        smem_desc_sw128(nslot(ps) + (uint32_t)k * 2048, 8192, 1024), idesc_acc, (!pfirst || k > 0));
+        tc_commit(smem_u32(&S.n_empty[ps % NS]));
+        if (plast) tc_commit(smem_u32(&S.acc_full));
+      };
+      for (; ok && it.next();) {
+        if (it.n == 0) continue;
+        ok = mbar_wait_bounded(smem_u32(&S.a_full[a & 1]), (uint32_t)((a / 2) & 1));
+        for (int j = 0; j < it.n && ok; ++j, ++s) {
+          ok = mbar_wait_bounded(smem_u32(&S.n_full[s % NS]), (uint32_t)((s / NS) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          // stage s & 1: the products of tile s - 2, which read it, were issued before
+          const uint32_t ts = tbase + (uint32_t)(s & 1) * 128;
+          const int nt = it.steps(j);
+          const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              tc_mma_f16(ts + 64 * w, smem_desc_sw128(abuf(a) + w * C::kA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                         smem_desc_sw128(nslot(s) + w * C::kN + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024), idesc_s,
+                         ks > 0);
+          tc_commit(smem_u32(&S.s_full[s & 1]));
+          if (j == it.n - 1) tc_commit(smem_u32(&S.a_empty[a & 1]));
+          products();
+          pend = true;
+          ps = s;
+          pa = a;
+          pnt = nt;
+          pfirst = j == 0;
+          plast = j == it.n - 1;
+        }
+        ++a;
+      }
+      if (ok) products();
+      // every MMA of this CTA has completed before tensor memory is freed
+      tc_commit(smem_u32(&S.done));
+      if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
+    }
+  } else if (warp == kWarpAux) {
+    int s = 0;
+    for (; ok && (clean || !kDq) && it.next();) {
+      for (int j = 0; j < it.n && ok; ++j, ++s) {
+        const int slot = s % NS;
+        if (kDq) {
+          uint32_t word[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int key = (it.n0 + j) * 64 + 32 * c + lane;
+            const bool on = key < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + key] != 0);
+            word[c] = __ballot_sync(0xffffffffu, on);
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.n_full[slot]), (uint32_t)((s / NS) & 1)));
+          if (!ok) break;
+          const int rows = 16 * it.steps(j);
+          unsigned char* k = sm + (nslot(s) - base);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (lane == 0) S.bits[slot][c] = word[c];
+            for (uint32_t off = ~word[c]; off != 0u; off &= off - 1) {  // one row at a time, 16 bytes a lane
+              const int r = 32 * c + __ffs(off) - 1;
+              if (r >= rows) break;
+              if (lane < D / 8)
+                *reinterpret_cast<uint4*>(k + (lane >> 3) * 8192 + sw128(r, lane & 7)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();  // generic writes -> MMA operand reads
+        } else {
+          const int row = (it.n0 + j) * 64 + 2 * lane;
+          const size_t g = (size_t)it.bk * p.N + row;
+          // rows past the end: probability zero
+          float2 nl = make_float2(-INFINITY, -INFINITY), de = make_float2(0.f, 0.f);
+          if (row < p.N) {
+            nl.x = neg_lse2(p.lse_in[g]);
+            de.x = p.delta[g];
+          }
+          if (row + 1 < p.N) {
+            nl.y = neg_lse2(p.lse_in[g + 1]);
+            de.y = p.delta[g + 1];
+          }
+          if (s >= NS)
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.n_empty[slot]), (uint32_t)((s / NS - 1) & 1)));
+          if (!ok) break;
+          S.side[slot][lane] = nl;
+          S.side[slot][32 + lane] = de;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.n_aux[slot]));
+      }
+    }
+  } else {
+    const int g = warp >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row of A = TMEM lane
+    const uint32_t trow = tbase + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t ts = trow + (uint32_t)g * 128, tacc = trow + C::kColAcc;
+    const float sc2 = p.scale * kLog2e;
+    const uint64_t sc2x2 = f2_make(sc2, sc2);
+    int a = 0, s = 0;
+    bool one = false;
+    auto wait = [&](uint64_t* bar, int phase) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
+      return ok;
+    };
+    for (; ok && it.next();) {
+      const int row = it.r0 + r;
+      if (kDq) {
+        // ---------------------------------------------------- dQ and Delta
+        const bool valid = row < p.N;
+        const size_t grow = (size_t)it.bk * p.N + row;
+        const size_t rows = (size_t)p.B * p.H * p.N;
+        if (it.new_b) {
+          one = sees_one(p, it.b, it.len);
+          if (tid == 0) p.alone[it.b] = one;
+        }
+        if (it.n == 0) {  // no keys (in this range)
+          if (g == 0 && valid) {
+            if (p.nks > 1) {
+              p.part_s[it.split * rows + grow] = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+              for (int c = 0; c < D / 8; ++c)
+                reinterpret_cast<uint4*>(static_cast<bf16*>(p.dq) + grow * D)[c] = make_uint4(0, 0, 0, 0);
+              p.delta[grow] = 0.f;
+            }
+          }
+          continue;
+        }
+        float nl = -INFINITY;  // rows past the end or without keys: probability zero
+        if (valid) nl = neg_lse2(p.lse_in[grow]);
+        const uint64_t nl2 = f2_make(nl, nl);
+        float c0 = 0.f;
+        uint64_t c2 = 0;
+        bool have_c = false;
+        uint64_t ls = f2_make(0.f, 0.f), ds = f2_make(0.f, 0.f);
+        for (int j = 0; j < it.n; ++j, ++s) {
+          if ((s & 1) != g) continue;
+          if (!wait(&S.s_full[g], s >> 1)) break;
+          if (clean && !wait(&S.n_aux[s % NS], s / NS)) break;
+          tc_fence_after();
+          if (j > 0 && !have_c) {  // the other group has the item's first tile
+            if (!wait(&S.c_full, a)) break;
+            c0 = S.q.c[r];
+            have_c = true;
+          }
+          c2 = f2_make(c0, c0);
+          const int nch = (it.steps(j) + 1) / 2;  // chunks of 32 keys
+#pragma unroll 1
+          for (int c = 0; c < nch; ++c) {
+            uint32_t bits;
+            if (clean) {
+              bits = S.bits[s % NS][c];
+            } else {
+              const int m = it.len - (it.n0 + j) * 64 - 32 * c;
+              bits = m >= 32 ? 0xffffffffu : (1u << m) - 1u;
+            }
+            float x[32], d[32];
+            tmem_ld32(ts + 32 * c, x);
+            tmem_ld32(ts + 64 + 32 * c, d);
+            tmem_wait_ld();
+            if (bits != 0xffffffffu) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (((bits >> i) & 1u) == 0u) {
+                  x[i] = -INFINITY;
+                  d[i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = f2_split(f2_fma(f2_make(x[2 * i], x[2 * i + 1]), sc2x2, nl2));
+              x[2 * i] = ex2_approx(e.x);
+              x[2 * i + 1] = ex2_approx(e.y);
+            }
+            if (!have_c) {
+              uint64_t w = f2_make(0.f, 0.f), wd = w;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t pp = f2_make(x[2 * i], x[2 * i + 1]);
+                w = f2_add(w, pp);
+                wd = f2_fma(pp, f2_make(d[2 * i], d[2 * i + 1]), wd);
+              }
+              const float2 u = f2_split(w), v = f2_split(wd);
+              const float sw = u.x + u.y;
+              c0 = sw > 1e-30f ? (v.x + v.y) / sw : 0.f;
+              if (!(fabsf(c0) < INFINITY)) c0 = 0.f;  // infinities and NaN of dP take their own way
+              c2 = f2_make(c0, c0);
+              have_c = true;
+              if (a > 0 && !wait(&S.x_read, a - 1)) break;
+              S.q.c[r] = c0;
+              mbar_arrive(smem_u32(&S.c_full));
+            }
+            uint32_t pk[16], dk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t pp = f2_make(x[2 * i], x[2 * i + 1]);
+              const uint64_t t = f2_mul(pp, f2_sub(f2_make(d[2 * i], d[2 * i + 1]), c2));
+              ls = f2_add(ls, pp);
+              ds = f2_add(ds, t);
+              const float2 tt = f2_split(t);
+              pk[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+              dk[i] = pack_bf16(tt.x, tt.y);
+            }
+            tmem_st16u(ts + 16 * c, pk);
+            tmem_st16u(ts + 64 + 16 * c, dk);
+          }
+          if (!ok) break;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&S.p_full[g]));
+        }
+        if (!ok) break;
+        // the row's sums of both groups
+        if (a > 0 && !wait(&S.x_read, a - 1)) break;
+        const float2 l2 = f2_split(ls), d2 = f2_split(ds);
+        S.q.sums[g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
+        mbar_arrive(smem_u32(&S.x_full));
+        if (!wait(&S.x_full, a)) break;
+        const float2 s0 = S.q.sums[0][r], s1 = S.q.sums[1][r];
+        c0 = S.q.c[r];
+        mbar_arrive(smem_u32(&S.x_read));
+        const float sp = s0.x + s1.x, sd = s0.y + s1.y;
+        const float delta = fmaf(c0, sp, sd), f = c0 - delta;
+        if (!wait(&S.acc_full, a)) break;
+        ++a;
+        tc_fence_after();
+        const float out = one ? 0.f : p.scale;
+#pragma unroll 1
+        for (int c = g * (D / 2); c < (g + 1) * (D / 2); c += 32) {
+          float x[32], y[32];
+          tmem_ld32(tacc + c, x);
+          tmem_ld32(tacc + D + c, y);
+          tmem_wait_ld();
+          if (!valid) continue;
+          if (p.nks > 1) {
+            const size_t at = (it.split * rows + grow) * D + c;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              *reinterpret_cast<float4*>(p.part_dq + at + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+              *reinterpret_cast<float4*>(p.part_dqb + at + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<bf16*>(p.dq) + grow * D + c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = one ? 0.f : fmaf(f, y[i], x[i]) * out;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                  pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&S.acc_free));
+        if (g == 0 && valid) {
+          if (p.nks > 1) p.part_s[it.split * rows + grow] = make_float4(c0, sp, sd, 1.f);
+          else p.delta[grow] = delta;
+        }
+      } else {
+        // ------------------------------------------------------- dK and dV
+        // keys that are not seen: whatever their rows hold, it stays in them
+        const bool seen = row < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + row] != 0);
+        bf16* dst = static_cast<bf16*>(g == 0 ? p.dv : p.dk) + ((size_t)it.bk * p.S + row) * D;
+        if (it.n == 0) {
+          if (p.nz == 1 && row < p.S)
+            for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        for (int j = 0; j < it.n; ++j, ++s) {
+          if ((s & 1) != g) continue;
+          if (!wait(&S.n_aux[s % NS], s / NS)) break;
+          if (!wait(&S.s_full[g], s >> 1)) break;
+          tc_fence_after();
+          const float2* side = S.side[s % NS];
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float x[32], d[32];
+            tmem_ld32(ts + 32 * c, x);
+            tmem_ld32(ts + 64 + 32 * c, d);
+            tmem_wait_ld();
+            uint32_t pk[16], dk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 nl = *reinterpret_cast<const float4*>(side + 16 * c + i);
+              const float4 de = *reinterpret_cast<const float4*>(side + 32 + 16 * c + i);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int e = 2 * (i + u);
+                const float2 t = f2_split(f2_fma(f2_make(x[e], x[e + 1]), sc2x2,
+                                                 u ? f2_make(nl.z, nl.w) : f2_make(nl.x, nl.y)));
+                const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
+                const float2 q = f2_split(f2_mul(f2_make(p0, p1), f2_sub(f2_make(d[e], d[e + 1]),
+                                                                         u ? f2_make(de.z, de.w) : f2_make(de.x, de.y))));
+                pk[i + u] = pack_bf16(p0, p1);
+                dk[i + u] = pack_bf16(q.x, q.y);
+              }
+            }
+            tmem_st16u(ts + 16 * c, pk);
+            tmem_st16u(ts + 64 + 16 * c, dk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&S.p_full[g]));
+        }
+        if (!ok) break;
+        if (!wait(&S.acc_full, a)) break;
+        ++a;
+        tc_fence_after();
+        const float f = g == 0 ? 1.f : (p.alone[it.b] != 0 ? 0.f : p.scale);
+        const uint32_t tsrc = tacc + (g == 0 ? D : 0);
+        float* part = g == 0 ? p.part_dv : p.part_dk;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float x[32];
+          tmem_ld32(tsrc + c, x);
+          tmem_wait_ld();
+          if (row >= p.S) continue;
+          if (p.nz > 1) {
+            float4* to = reinterpret_cast<float4*>(part + (((size_t)it.i * p.nz + it.slot) * 128 + r) * D + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          } else {
+            uint4* to = reinterpret_cast<uint4*>(dst + c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = seen && f != 0.f ? x[i] * f : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              to[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                 pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&S.acc_free));
+      }
+    }
+  }
+
+  if (!ok) report_status(p.status, LLSA_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// The first pass's splits of a row joined: a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_dq_join(CrossParams p) {
+  constexpr int C = D / 32;
+  const size_t rows = (size_t)p.B * p.H * p.N;
+  const size_t row = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  float delta = 0.f;
+  for (int z = 0; z < p.nks; ++z) {
+    const float4 s = p.part_s[z * rows + row];
+    delta += fmaf(s.x, s.y, s.z);
+  }
+  float acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  for (int z = 0; z < p.nks; ++z) {
+    const float4 s = p.part_s[z * rows + row];
+    if (s.w == 0.f) continue;  // a split without keys: its parts are not written
+    const float f = s.x - delta;
+    const size_t at = (z * rows + row) * D + lane * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += fmaf(f, p.part_dqb[at + c], p.part_dq[at + c]);
+  }
+  const bool one = p.alone[row / ((size_t)p.H * p.N)] != 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    store_elem(static_cast<bf16*>(p.dq) + row * D + lane * C + c, one ? 0.f : acc[c] * p.scale);
+  if (lane == 0) p.delta[row] = delta;
+}
+
+// The second pass's shares of a key tile summed: D / 4 threads per key and
+// tensor (blockIdx.y: dV, dK).
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_dkv_join(CrossParams p, int grid) {
+  constexpr int T = D / 4;
+  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t krow = at / T;
+  const int c = (int)(at % T) * 4;
+  if (krow >= (size_t)p.B * p.H * p.S) return;
+  const int bk = (int)(krow / p.S), key = (int)(krow - (size_t)bk * p.S), b = bk / p.H;
+  const bool is_k = blockIdx.y != 0;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (key < cross_len(p, b) && (p.mask == nullptr || p.mask[(size_t)b * p.S + key] != 0) &&
+      !(is_k && p.alone[b] != 0)) {
+    const CrossPairs w((long long)p.B * p.H, p.N, p.S, p.nz, grid);
+    const long long u = (long long)bk * ((p.S + 127) / 128) + key / 128;
+    const int n = w.cta_of(u * w.nq + w.nq - 1) - w.cta_of(u * w.nq) + 1;
+    const float* src = (is_k ? p.part_dk : p.part_dv) + ((size_t)u * p.nz * 128 + key % 128) * D + c;
+    for (int z = 0; z < n; ++z) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (size_t)z * 128 * D);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    const float f = is_k ? p.scale : 1.f;
+    s.x *= f;
+    s.y *= f;
+    s.z *= f;
+    s.w *= f;
+  }
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<bf16*>(is_k ? p.dk : p.dv) + krow * D + c);
+  *dst = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+template <int D, bool kDq>
+cudaError_t launch_pass(const CrossParams& p, const CUtensorMap* a, const CUtensorMap* n, int grid, cudaStream_t s) {
+  constexpr size_t smem = Cfg<D>::kEnd + sizeof(Shared<Cfg<D>::kSlots>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  cudaError_t e =
+      cudaFuncSetAttribute(cross_bwd_tc_kernel<D, kDq>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cross_bwd_tc_kernel<D, kDq><<<grid, kThreads, smem, s>>>(a[0], a[1], n[0], n[1], p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_typed(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,
+                         const CUtensorMap* kv128, const CUtensorMap* q64, cudaStream_t s) {
+  const long long items = (long long)p.B * p.H * p.nks * ((p.N + 127) / 128);
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pass<D, true>(p, q128, kv64, (int)(items < kCrossSms ? items : kCrossSms), s);
+  const size_t rows = (size_t)p.B * p.H * p.N;
+  if (e == cudaSuccess && p.nks > 1) {
+    cross_dq_join<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess || p.S == 0) return e;
+  const int grid = CrossPairs::grid_of((long long)p.B * p.H, p.N, p.S, p.nz);
+  e = launch_pass<D, false>(p, kv128, q64, grid, s);
+  if (e == cudaSuccess && p.nz > 1) {
+    const size_t threads = (size_t)p.B * p.H * p.S * (D / 4);
+    cross_dkv_join<D><<<dim3((unsigned)((threads + 255) / 256), 2), 256, 0, s>>>(p, grid);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace
+
+CrossPlan cross_tc_bwd_plan(long long BH, int N, int S) {
+  const long long units = BH * (((long long)N + 127) / 128), kt = ((long long)S + 63) / 64;
+  long long nks = kCrossSms / units;
+  if (nks > kt) nks = kt;
+  return {nks < 1 ? 1 : (int)nks, CrossPairs::slots(BH, N, S)};
+}
+
+cudaError_t launch_cross_bwd_tc(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,
+                                const CUtensorMap* kv128, const CUtensorMap* q64, cudaStream_t s) {
+  return p.D == 64 ? launch_typed<64>(p, q128, kv64, kv128, q64, s) : launch_typed<128>(p, q128, kv64, kv128, q64, s);
+}
+
+}  // namespace llsa
