@@ -26,7 +26,7 @@
 //
 //   warps 0-3, 4-7  the two groups, also the epilogue;
 //   warp 8          TMA loads of A (two buffers) and N (a ring);
-//   warp 9          one thread issues the MMAs;
+//   warp 9          issues the MMAs;
 //   warp 10         first pass: with lengths or a mask, the bits of the keys
 //                   seen and zeros over the K rows that are not (their dS is
 //                   zero, and zero times NaN is NaN); second pass: lse and
@@ -236,67 +236,71 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         if (!mbar_wait_bounded(smem_u32(&S.n_full[i % NS]), (uint32_t)((i / NS) & 1))) ok = false;
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1, 0);
-      constexpr uint32_t kSecond = kDq ? 0 : C::kN;  // accB's right side: N1 or N2
-      int a = 0, s = 0;
-      bool pend = false, pfirst = false, plast = false;
-      int ps = 0, pa = 0, pnt = 0;   // the pending products' tile, item and 16-row steps
-      auto products = [&]() {        // accA (+)= dS N1, accB (+)= P N1 or N2
-        if (!pend) return;
-        pend = false;
-        const int g = ps & 1;
-        if (kDq && clean) ok = mbar_wait_bounded(smem_u32(&S.n_aux[ps % NS]), (uint32_t)((ps / NS) & 1));
-        if (ok) ok = mbar_wait_bounded(smem_u32(&S.p_full[g]), (uint32_t)((ps >> 1) & 1));
-        if (ok && pfirst && pa > 0) ok = mbar_wait_bounded(smem_u32(&S.acc_free), (uint32_t)((pa - 1) & 1));
-        if (!ok) return;
+    // the whole warp walks; one lane issues
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1, 0);
+    constexpr uint32_t kSecond = kDq ? 0 : C::kN;  // accB's right side: N1 or N2
+    const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, 8192, 1024);
+    const uint32_t lead = elect_lane();
+    int a = 0, s = 0;
+    bool pend = false, pfirst = false, plast = false;
+    int ps = 0, pa = 0, pnt = 0;   // the pending products' tile, item and 16-row steps
+    auto wait = [&](uint64_t* bar, int phase) {
+      return ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
+    };
+    auto products = [&]() {        // accA (+)= dS N1, accB (+)= P N1 or N2
+      if (!pend) return;
+      pend = false;
+      const int g = ps & 1;
+      if (kDq && clean && !wait(&S.n_aux[ps % NS], ps / NS)) return;
+      if (!wait(&S.p_full[g], ps >> 1)) return;
+      if (pfirst && pa > 0 && !wait(&S.acc_free, pa - 1)) return;
+      tc_fence_after();
+      const uint32_t ts = tbase + (uint32_t)g * 128;
+      const uint64_t n1 = desc_at(nmaj, nslot(ps)), n2 = desc_at(n1, kSecond);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= pnt) break;
+        const uint32_t add = !pfirst || k > 0;
+        tc_mma_f16_ts_by(lead, tbase + C::kColAcc + D, ts + k * 8, desc_at(n2, k * 2048), idesc_acc, add);
+        tc_mma_f16_ts_by(lead, tbase + C::kColAcc, ts + 64 + k * 8, desc_at(n1, k * 2048), idesc_acc, add);
+      }
+      tc_commit_by(lead, smem_u32(&S.n_empty[ps % NS]));
+      if (plast) tc_commit_by(lead, smem_u32(&S.acc_full));
+    };
+    for (; ok && it.next();) {
+      if (it.n == 0) continue;
+      wait(&S.a_full[a & 1], a / 2);
+      const uint64_t a1 = desc_at(kmaj, abuf(a));
+      for (int j = 0; j < it.n && ok; ++j, ++s) {
+        if (!wait(&S.n_full[s % NS], s / NS)) break;
         tc_fence_after();
-        const uint32_t ts = tbase + (uint32_t)g * 128;
-        for (int k = 0; k < pnt; ++k)
-          tc_mma_f16_ts(tbase + C::kColAcc + D, ts + (uint32_t)k * 8,
-                        smem_desc_sw128(nslot(ps) + kSecond + (uint32_t)k * 2048, 8192, 1024), idesc_acc,
-                        (!pfirst || k > 0));
-        for (int k = 0; k < pnt; ++k)
-          tc_mma_f16_ts(tbase + C::kColAcc, ts + 64 + (uint32_t)k * 8,
-                        smem_desc_sw128(nslot(ps) + (uint32_t)k * 2048, 8192, 1024), idesc_acc, (!pfirst || k > 0));
-        tc_commit(smem_u32(&S.n_empty[ps % NS]));
-        if (plast) tc_commit(smem_u32(&S.acc_full));
-      };
-      for (; ok && it.next();) {
-        if (it.n == 0) continue;
-        ok = mbar_wait_bounded(smem_u32(&S.a_full[a & 1]), (uint32_t)((a / 2) & 1));
-        for (int j = 0; j < it.n && ok; ++j, ++s) {
-          ok = mbar_wait_bounded(smem_u32(&S.n_full[s % NS]), (uint32_t)((s / NS) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          // stage s & 1: the products of tile s - 2, which read it, were issued before
-          const uint32_t ts = tbase + (uint32_t)(s & 1) * 128;
-          const int nt = it.steps(j);
-          const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
+        // stage s & 1: the products of tile s - 2, which read it, were issued before
+        const uint32_t ts = tbase + (uint32_t)(s & 1) * 128;
+        const int nt = it.steps(j);
+        const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
+        const uint64_t n1 = desc_at(kmaj, nslot(s));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc_mma_f16(ts + 64 * w, smem_desc_sw128(abuf(a) + w * C::kA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                         smem_desc_sw128(nslot(s) + w * C::kN + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024), idesc_s,
-                         ks > 0);
-          tc_commit(smem_u32(&S.s_full[s & 1]));
-          if (j == it.n - 1) tc_commit(smem_u32(&S.a_empty[a & 1]));
-          products();
-          pend = true;
-          ps = s;
-          pa = a;
-          pnt = nt;
-          pfirst = j == 0;
-          plast = j == it.n - 1;
-        }
-        ++a;
+            tc_mma_f16_by(lead, ts + 64 * w, desc_at(a1, w * C::kA + (ks >> 2) * 16384 + (ks & 3) * 32),
+                          desc_at(n1, w * C::kN + (ks >> 2) * 8192 + (ks & 3) * 32), idesc_s, ks > 0);
+        tc_commit_by(lead, smem_u32(&S.s_full[s & 1]));
+        if (j == it.n - 1) tc_commit_by(lead, smem_u32(&S.a_empty[a & 1]));
+        products();
+        pend = true;
+        ps = s;
+        pa = a;
+        pnt = nt;
+        pfirst = j == 0;
+        plast = j == it.n - 1;
       }
-      if (ok) products();
-      // every MMA of this CTA has completed before tensor memory is freed
-      tc_commit(smem_u32(&S.done));
-      if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
+      ++a;
     }
+    if (ok) products();
+    // every MMA of this CTA has completed before tensor memory is freed
+    tc_commit_by(lead, smem_u32(&S.done));
+    if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
   } else if (warp == kWarpAux) {
     int s = 0;
     for (; ok && (clean || !kDq) && it.next();) {

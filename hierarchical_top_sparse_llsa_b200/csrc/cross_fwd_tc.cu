@@ -12,7 +12,7 @@
 //   warp 8          TMA loads: Q tiles into a ring of slots, K and V tiles
 //                   into another.  Key tiles that fit in the ring are loaded
 //                   once and stay for all items of the same keys;
-//   warp 9          one thread issues the MMAs: S_w = Q_w K^T into tensor
+//   warp 9          issues the MMAs: S_w = Q_w K^T into tensor
 //                   memory, and O_w += P_w V with P_w read from tensor memory
 //                   (over S_w, which the softmax has read);
 //   warp 10         with lengths or a mask: the bits of the keys seen in each
@@ -139,70 +139,78 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         if (!mbar_wait_bounded(smem_u32(&S.kv_full[i % C::kKv]), (uint32_t)((i / C::kKv) & 1))) ok = false;
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      const uint32_t idesc_pv = idesc_bf16_f32(128, D, 1, 0);
-      int t = 0, f = 0, frun = 0;
-      int np[2] = {0, 0};      // P tiles taken
-      bool pend[2] = {false, false};
-      int pf = 0, pnt = 0;     // the pending product's V tile and its 16-key steps
-      bool pfirst = false, plast = false, pfree = false;
-      auto pv = [&](int w) {   // O_w (+)= P_w V of the previous step
-        if (!pend[w]) return;
-        pend[w] = false;
-        ok = mbar_wait_bounded(smem_u32(&S.kv_full[pf % C::kKv]), (uint32_t)((pf / C::kKv) & 1));
-        if (ok && clean) ok = mbar_wait_bounded(smem_u32(&S.kv_clean[pf % C::kKv]), (uint32_t)((pf / C::kKv) & 1));
-        if (ok) ok = mbar_wait_bounded(smem_u32(&S.p_full[w]), (uint32_t)(np[w] & 1));
-        if (!ok) return;
-        ++np[w];
-        tc_fence_after();
-        for (int k = 0; k < pnt; ++k)
-          tc_mma_f16_ts(tbase + C::kColO + (uint32_t)w * D, tbase + (uint32_t)w * 128 + (uint32_t)k * 8,
-                        smem_desc_sw128(kvslot(pf) + (uint32_t)k * 2048, 16384, 1024), idesc_pv, (!pfirst || k > 0));
-        if (plast) tc_commit(smem_u32(&S.o_full[w]));
-      };
-      for (; ok && it.next();) {
-        if (it.nkt == 0) continue;
-        if (!it.resident || it.new_run) {
-          frun = f;
-          f += 2 * it.nkt;
-        }
-        const int t0 = t;
-        t += it.act1 ? 2 : 1;
-        for (int j = 0; j < it.nkt && ok; ++j) {
-          const int fk = frun + 2 * j;
-          const int nt = it.steps(j);
-          const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
-          ok = mbar_wait_bounded(smem_u32(&S.kv_full[fk % C::kKv]), (uint32_t)((fk / C::kKv) & 1));
-          for (int w = 0; w < 2 && ok; ++w) {
-            pv(w);
-            if (!ok || (w == 1 && !it.act1)) continue;
-            const int tw = t0 + w;
-            if (j == 0) ok = mbar_wait_bounded(smem_u32(&S.q_full[tw % C::kQ]), (uint32_t)((tw / C::kQ) & 1));
-            if (!ok) break;
-            tc_fence_after();
+    // the whole warp walks; one lane issues
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1, 0);
+    const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, 16384, 1024);
+    const uint32_t lead = elect_lane();
+    int t = 0, f = 0, frun = 0;
+    int np[2] = {0, 0};      // P tiles taken
+    bool pend[2] = {false, false};
+    int pf = 0, pnt = 0;     // the pending product's V tile and its 16-key steps
+    bool pfirst = false, plast = false, pfree = false;
+    auto wait = [&](uint64_t* bar, int phase) {
+      return ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
+    };
+    auto pv = [&](int w) {   // O_w (+)= P_w V of the previous step
+      if (!pend[w]) return;
+      pend[w] = false;
+      if (!wait(&S.kv_full[pf % C::kKv], pf / C::kKv)) return;
+      if (clean && !wait(&S.kv_clean[pf % C::kKv], pf / C::kKv)) return;
+      if (!wait(&S.p_full[w], np[w])) return;
+      ++np[w];
+      tc_fence_after();
+      const uint64_t v = desc_at(nmaj, kvslot(pf));
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc_mma_f16(tbase + (uint32_t)w * 128,
-                         smem_desc_sw128(qslot(tw) + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                         smem_desc_sw128(kvslot(fk) + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0);
-            tc_commit(smem_u32(&S.s_full[w]));
-            pend[w] = true;
-          }
-          if (!ok) break;
-          if (pfree) tc_commit(smem_u32(&S.kv_empty[pf % C::kKv]));
-          pf = fk + 1;
-          pnt = nt;
-          pfirst = j == 0;
-          plast = j == it.nkt - 1;
-          pfree = !it.resident || it.last_of_run;
-          if (pfree) tc_commit(smem_u32(&S.kv_empty[fk % C::kKv]));
-        }
+      for (int k = 0; k < 8; ++k) {
+        if (k >= pnt) break;
+        tc_mma_f16_ts_by(lead, tbase + C::kColO + w * D, tbase + w * 128 + k * 8, desc_at(v, k * 2048), idesc_pv,
+                         !pfirst || k > 0);
       }
-      for (int w = 0; w < 2 && ok; ++w) pv(w);
-      // every MMA of this CTA has completed before tensor memory is freed
-      tc_commit(smem_u32(&S.done));
-      if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
+      if (plast) tc_commit_by(lead, smem_u32(&S.o_full[w]));
+    };
+    for (; ok && it.next();) {
+      if (it.nkt == 0) continue;
+      if (!it.resident || it.new_run) {
+        frun = f;
+        f += 2 * it.nkt;
+      }
+      const int t0 = t;
+      t += it.act1 ? 2 : 1;
+      for (int j = 0; j < it.nkt && ok; ++j) {
+        const int fk = frun + 2 * j;
+        const int nt = it.steps(j);
+        const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
+        const uint64_t k = desc_at(kmaj, kvslot(fk));
+        if (!wait(&S.kv_full[fk % C::kKv], fk / C::kKv)) break;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (ok) pv(w);
+          if (!ok || (w == 1 && !it.act1)) continue;
+          const int tw = t0 + w;
+          if (j == 0 && !wait(&S.q_full[tw % C::kQ], tw / C::kQ)) continue;
+          tc_fence_after();
+          const uint64_t q = desc_at(kmaj, qslot(tw));
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc_mma_f16_by(lead, tbase + w * 128, desc_at(q, (ks >> 2) * 16384 + (ks & 3) * 32),
+                          desc_at(k, (ks >> 2) * 16384 + (ks & 3) * 32), idesc_s, ks > 0);
+          tc_commit_by(lead, smem_u32(&S.s_full[w]));
+          pend[w] = true;
+        }
+        if (!ok) break;
+        if (pfree) tc_commit_by(lead, smem_u32(&S.kv_empty[pf % C::kKv]));
+        pf = fk + 1;
+        pnt = nt;
+        pfirst = j == 0;
+        plast = j == it.nkt - 1;
+        pfree = !it.resident || it.last_of_run;
+        if (pfree) tc_commit_by(lead, smem_u32(&S.kv_empty[fk % C::kKv]));
+      }
     }
+    for (int w = 0; w < 2 && ok; ++w) pv(w);
+    // every MMA of this CTA has completed before tensor memory is freed
+    tc_commit_by(lead, smem_u32(&S.done));
+    if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
   } else if (warp == kWarpClean) {
     if (clean) {
       int f = 0;

@@ -14,6 +14,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // with 128-byte swizzle (the TMA layout of every tile here).
 __device__ __forceinline__ uint32_t sw128(int r, int jj) { return (uint32_t)(r * 128 + ((jj ^ (r & 7)) << 4)); }
 
+// Descriptor of an operand tile at shared address a, given that of address 0
+// (addresses stay below 2^18, so the field takes the sum).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc0, uint32_t a) { return desc0 + (a >> 4); }
+
 // The items of a CTA, in order: 256 query rows of one key head against one
 // range of its key tiles.  Every warp role walks them by itself; rows are
 // innermost, so items of the same keys follow one another (a run).
