@@ -435,9 +435,9 @@ int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* 
   }
   const cudaStream_t s = (cudaStream_t)stream;
   if (desc->dtype == LLSA_BF16) {
-    CUtensorMap q128[2], q64[2], kv128[2], kv64[2];
-    const void* const rows_of[2] = {q, dout};
-    st = make_query_maps(q128, desc, rows_of, 2, 128);
+    CUtensorMap q128[3], q64[2], kv128[2], kv64[2];
+    const void* const rows_of[3] = {q, dout, dq};
+    st = make_query_maps(q128, desc, rows_of, 3, 128);
     if (st == LLSA_OK) st = make_query_maps(q64, desc, rows_of, 2, 64);
     if (st == LLSA_OK) st = make_key_maps(kv128, desc, k, v, q, 128);
     if (st == LLSA_OK) st = make_key_maps(kv64, desc, k, v, q, 64);

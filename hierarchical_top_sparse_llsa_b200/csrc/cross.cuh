@@ -92,7 +92,7 @@ struct CrossPairs {
 
 // maps: Q, K, V, O as 3D [B H, rows, D] bf16, box 128 rows x 64 columns, 128-byte swizzle
 cudaError_t launch_cross_fwd_tc(const CrossParams& p, const CUtensorMap* maps, cudaStream_t s);
-// q128, kv64, kv128, q64: (Q, dO) or (K, V) as above, boxes of 128 or 64 rows
+// q128, kv64, kv128, q64: (Q, dO) or (K, V) as above, boxes of 128 or 64 rows; q128[2]: dQ
 cudaError_t launch_cross_bwd_tc(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,
                                 const CUtensorMap* kv128, const CUtensorMap* q64, cudaStream_t s);
 cudaError_t launch_cross_fwd_simt(const CrossParams& p, int dtype, cudaStream_t s);

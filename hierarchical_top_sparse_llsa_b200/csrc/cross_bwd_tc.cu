@@ -10,27 +10,29 @@
 //   S = A1 N1^T, dP = A2 N2^T     into tensor memory,
 //   P and dS                      bf16, over them in tensor memory,
 //   accA += dS N1, accB += P N1 (first pass) or P N2 (second pass),
-// so neither P nor dS goes through shared memory.  Two stages of S and dP
-// alternate between two groups of four warps, one thread per row: the tensor
-// cores fill one while the exponentials of the other are computed.
+// so neither P nor dS goes through shared memory.
 //
 // Delta is formed from unrounded terms and in the same walk as dQ.  With any
 // number c per row, dS = P (dP - c) + P (c - Delta), so
 //   dQ = scale (sum_j P (dP - c) K + (c - Delta) sum_j P K),
 //   Delta = c sum_j P + sum_j P (dP - c);
-// c, the mean of dP over the first 32 keys weighted with P, is near Delta, so
-// the rounding of P (dP - c) to bf16 is that of dS, and all of it is exact in
-// c.  (Delta from the stored O would carry O's rounding to bf16, which the
-// keys' common part lifts above the gradient where many keys share a row.)
+// c, the mean of dP over the first keys, takes off what the values have in
+// common, so the rounding of P (dP - c) to bf16 is that of dS, and all of it is
+// exact in c.  (Delta from the stored O would carry O's rounding to bf16, which
+// the keys' common part lifts above the gradient where many keys share a row.)
 // A query that sees one key alone has dS = 0: P is 1 whatever the score.
 //
-//   warps 0-3, 4-7  the two groups, also the epilogue;
-//   warp 8          TMA loads of A (two buffers) and N (a ring);
-//   warp 9          issues the MMAs;
-//   warp 10         first pass: with lengths or a mask, the bits of the keys
-//                   seen and zeros over the K rows that are not (their dS is
-//                   zero, and zero times NaN is NaN); second pass: lse and
-//                   Delta of the queries that stream by.
+// S and dP have kStages stages in tensor memory, each with a group of four
+// warps, one thread per row; the tensor cores fill one while the exponentials
+// of the others are computed.  Warps:
+//   the groups' first;
+//   four for the epilogue, so that the groups go on with the next item;
+//   load    TMA loads of A (two buffers) and N (a ring);
+//   mma     issues the MMAs;
+//   aux     first pass: with lengths or a mask, the bits of the keys seen and
+//           zeros over the K rows that are not (their dS is zero, and zero
+//           times NaN is NaN); second pass: lse and Delta of the queries that
+//           stream by.
 // The second pass cuts all its (key tile, query tile) pairs into equal runs,
 // one per SM; a key tile that several SMs share is summed by a last kernel, in
 // a fixed order.  The first pass cuts the keys where there are few rows.
@@ -45,31 +47,35 @@ namespace llsa {
 
 namespace {
 
-constexpr int kThreads = 352;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpAux = 10;
-
 template <int D>
 struct Cfg {
+  // tensor memory has 512 columns: accA and accB take 2 D, a stage 128
+  static constexpr int kStages = (D == 64) ? 3 : 2;
+  static constexpr int kEpi = kStages * 4;  // first epilogue warp
+  static constexpr int kLoad = kEpi + 4, kMma = kLoad + 1, kAux = kMma + 1;
+  static constexpr int kThreads = (kAux + 1) * 32;
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
   static constexpr int kSlots = (D == 64) ? 6 : 3;
+  static constexpr int kSums = (D == 64) ? 2 : 1;  // items whose row sums are held
   static constexpr int kOffN = 4 * kA;     // two buffers of A1, A2
   static constexpr int kEnd = kOffN + kSlots * 2 * kN;
-  static constexpr uint32_t kColAcc = 256;  // S_0 dP_0 | S_1 dP_1 | accA | accB
+  static constexpr uint32_t kColAcc = 128 * kStages;  // S | dP of each stage, accA | accB
 };
 
-template <int NS>
+template <typename C>
 struct Shared {
-  uint64_t a_full[2], a_empty[2], n_full[NS], n_empty[NS], n_aux[NS];
-  uint64_t s_full[2], p_full[2], acc_full, acc_free, c_full, x_full, x_read, done;
+  uint64_t a_full[2], a_empty[2], n_full[C::kSlots], n_empty[C::kSlots], n_aux[C::kSlots];
+  uint64_t s_full[C::kStages], p_full[C::kStages], acc_full, acc_free, staged, done;
+  uint64_t c_full[C::kSums], x_full[C::kSums], x_read[C::kSums];
   uint32_t tmem_base;
-  uint32_t bits[NS][2];  // first pass: keys seen, by slot
+  uint32_t bits[C::kSlots][2];  // first pass: keys seen, by slot
   union alignas(16) {
     struct {
-      float c[128];          // of the item's rows
-      float2 sums[2][128];   // each group's sum P, sum P (dP - c)
+      float c[C::kSums][128];                  // of the item's rows
+      float2 sums[C::kSums][C::kStages][128];  // each group's sum P, sum P (dP - c)
     } q;
-    float2 side[NS][64];     // second pass, by slot: [0..31] -lse of 64 queries, [32..63] their Delta
+    float2 side[C::kSlots][64];  // second pass, by slot: [0..31] -lse of 64 queries, [32..63] their Delta
   };
 };
 
@@ -82,9 +88,8 @@ struct BwdItems {
   CrossPairs w;                // second pass
   int i, end, nt;              // kDq: items; else units (key tiles); nt: row tiles per head
   long long beg, fin;          // second pass: the CTA's pairs
-  int bk, b, split, slot, r0, len;
+  int bk, b, split, slot, tile, r0, len;
   int n0, n;                   // first tile of 64 streamed rows, how many
-  bool new_b;
 
   __device__ __forceinline__ BwdItems(const CrossParams& p_)
       : p(p_), w((long long)p_.B * p_.H, p_.N, p_.S, p_.nz, (int)gridDim.x), b(-1) {
@@ -100,24 +105,38 @@ struct BwdItems {
       i = (int)(beg / w.nq) - 1;
       end = (int)((fin + w.nq - 1) / w.nq);
     }
-  }
-  __device__ __forceinline__ bool next() {
-    if (++i >= end) return false;
-    const int run = i / nt;
-    r0 = (i - run * nt) * 128;
+    const int run = (i + 1) / nt;
+    tile = i - run * nt;  // of the item before the first
+    split = kDq ? run % p.nks : 0;
     bk = kDq ? run / p.nks : run;
+    range();
+  }
+  // what the head and the range of the keys settle
+  __device__ __forceinline__ void range() {
     const int nb = bk / p.H;
-    new_b = nb != b;
-    if (new_b) {
+    if (nb >= p.B) return;  // past the last item
+    if (nb != b) {
       b = nb;
       len = cross_len(p, b);
     }
     if (kDq) {
-      split = run - bk * p.nks;
       const int kt = (len + 63) / 64;
-      n0 = (int)((long long)kt * split / p.nks);
-      n = (int)((long long)kt * (split + 1) / p.nks) - n0;
-    } else {
+      n0 = p.nks == 1 ? 0 : (int)((long long)kt * split / p.nks);
+      n = (p.nks == 1 ? kt : (int)((long long)kt * (split + 1) / p.nks)) - n0;
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (++i >= end) return false;
+    if (++tile == nt) {
+      tile = 0;
+      if (!kDq || ++split == p.nks) {
+        split = 0;
+        ++bk;
+      }
+      range();
+    }
+    r0 = tile * 128;
+    if (!kDq) {
       const long long u = (long long)i * w.nq;
       n0 = (int)(beg > u ? beg - u : 0);
       n = (int)(fin < u + w.nq ? fin - u : w.nq) - n0;
@@ -125,6 +144,13 @@ struct BwdItems {
       if (r0 >= len) n = 0;  // no key of the tile is seen
     }
     return true;
+  }
+  // the query row that row r of the next item is (its head's first where there is none)
+  __device__ __forceinline__ size_t peek(int r) const {
+    const bool same = tile + 1 < nt;
+    const int nbk = same || split + 1 < p.nks ? bk : bk + 1;
+    const int row = same ? (tile + 1) * 128 + r : r;
+    return (size_t)(i + 1 < end ? nbk : bk) * p.N + (row < p.N ? row : 0);
   }
   // 16-row steps of the item's tile j
   __device__ __forceinline__ int steps(int j) const {
@@ -157,27 +183,29 @@ __device__ __forceinline__ bool sees_one(const CrossParams& p, int b, int len) {
 }
 
 template <int D, bool kDq>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap ta2,
-                    const __grid_constant__ CUtensorMap tn1, const __grid_constant__ CUtensorMap tn2, CrossParams p) {
+                    const __grid_constant__ CUtensorMap tn1, const __grid_constant__ CUtensorMap tn2,
+                    const __grid_constant__ CUtensorMap tdq, CrossParams p) {
   using C = Cfg<D>;
   constexpr int H = D / 64;  // 64-column halves of a tile
-  constexpr int NS = C::kSlots;
+  constexpr int NS = C::kSlots, NG = C::kStages;
   extern __shared__ __align__(1024) unsigned char sm[];
-  using Sh = Shared<NS>;
-  Sh& S = *reinterpret_cast<Sh*>(sm + C::kEnd);
+  Shared<C>& S = *reinterpret_cast<Shared<C>*>(sm + C::kEnd);
   const uint32_t base = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const bool clean = kDq && (p.mask != nullptr || p.kv_len != nullptr);
   bool ok = true;
 
-  if (warp == kWarpMma) {
+  if (warp == C::kMma) {
     tmem_alloc(smem_u32(&S.tmem_base), 512);
     tmem_relinquish();
   } else if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&S.a_full[i]), 1);
       mbar_init(smem_u32(&S.a_empty[i]), 1);
+    }
+    for (int i = 0; i < NG; ++i) {
       mbar_init(smem_u32(&S.s_full[i]), 1);
       mbar_init(smem_u32(&S.p_full[i]), 128);
     }
@@ -187,22 +215,28 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       mbar_init(smem_u32(&S.n_aux[i]), 1);
     }
     mbar_init(smem_u32(&S.acc_full), 1);
-    mbar_init(smem_u32(&S.acc_free), 256);
-    mbar_init(smem_u32(&S.c_full), 128);
-    mbar_init(smem_u32(&S.x_full), 256);
-    mbar_init(smem_u32(&S.x_read), 256);
+    mbar_init(smem_u32(&S.acc_free), 128);
+    mbar_init(smem_u32(&S.staged), 128);
+    for (int i = 0; i < C::kSums; ++i) {
+      mbar_init(smem_u32(&S.c_full[i]), 128);
+      mbar_init(smem_u32(&S.x_full[i]), NG * 128);
+      mbar_init(smem_u32(&S.x_read[i]), 128);
+    }
     mbar_init(smem_u32(&S.done), 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = S.tmem_base;
+  const uint32_t tbase = uniform(S.tmem_base);
   auto abuf = [&](int a) { return base + (uint32_t)(a & 1) * 2 * C::kA; };
   auto nslot = [&](int s) { return base + C::kOffN + (uint32_t)(s % NS) * 2 * C::kN; };
+  auto wait = [&](uint64_t* bar, int phase) {  // by whole warps
+    return ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
+  };
   BwdItems<kDq> it(p);
 
-  if (warp == kWarpLoad) {
+  if (warp == C::kLoad) {
     if (lane == 0) {
       int a = 0, s = 0;  // items and streamed tiles so far
       for (; ok && it.next();) {
@@ -235,73 +269,70 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       for (int i = s > NS ? s - NS : 0; i < s; ++i)
         if (!mbar_wait_bounded(smem_u32(&S.n_full[i % NS]), (uint32_t)((i / NS) & 1))) ok = false;
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp == C::kMma) {
     // the whole warp walks; one lane issues
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1, 0);
     constexpr uint32_t kSecond = kDq ? 0 : C::kN;  // accB's right side: N1 or N2
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, 8192, 1024);
     const uint32_t lead = elect_lane();
-    int a = 0, s = 0;
-    bool pend = false, pfirst = false, plast = false;
-    int ps = 0, pa = 0, pnt = 0;   // the pending products' tile, item and 16-row steps
-    auto wait = [&](uint64_t* bar, int phase) {
-      return ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
-    };
-    auto products = [&]() {        // accA (+)= dS N1, accB (+)= P N1 or N2
-      if (!pend) return;
-      pend = false;
-      const int g = ps & 1;
+    int a = 0, s = 0;        // items; tiles whose S and dP are issued
+    int ps = 0, pa = 0;      // tiles, and items, whose products are
+    uint32_t queue = 0;      // of the tiles in between, the oldest on top of the lowest byte: 16-row steps | first | last
+    auto products = [&]() {  // accA (+)= dS N1, accB (+)= P N1 or N2 of tile ps
+      const uint32_t info = (queue >> (8 * (s - ps - 1))) & 255u;
+      const int g = ps % NG, pnt = (int)(info & 7u);
+      const bool first = (info & 8u) != 0;
       if (kDq && clean && !wait(&S.n_aux[ps % NS], ps / NS)) return;
-      if (!wait(&S.p_full[g], ps >> 1)) return;
-      if (pfirst && pa > 0 && !wait(&S.acc_free, pa - 1)) return;
+      if (!wait(&S.p_full[g], ps / NG)) return;
+      if (first) {
+        if (pa > 0 && !wait(&S.acc_free, pa - 1)) return;
+        ++pa;
+      }
       tc_fence_after();
       const uint32_t ts = tbase + (uint32_t)g * 128;
       const uint64_t n1 = desc_at(nmaj, nslot(ps)), n2 = desc_at(n1, kSecond);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (k >= pnt) break;
-        const uint32_t add = !pfirst || k > 0;
+        const uint32_t add = !first || k > 0;
         tc_mma_f16_ts_by(lead, tbase + C::kColAcc + D, ts + k * 8, desc_at(n2, k * 2048), idesc_acc, add);
         tc_mma_f16_ts_by(lead, tbase + C::kColAcc, ts + 64 + k * 8, desc_at(n1, k * 2048), idesc_acc, add);
       }
       tc_commit_by(lead, smem_u32(&S.n_empty[ps % NS]));
-      if (plast) tc_commit_by(lead, smem_u32(&S.acc_full));
+      if ((info & 16u) != 0) tc_commit_by(lead, smem_u32(&S.acc_full));
+      ++ps;
     };
     for (; ok && it.next();) {
-      if (it.n == 0) continue;
-      wait(&S.a_full[a & 1], a / 2);
-      const uint64_t a1 = desc_at(kmaj, abuf(a));
-      for (int j = 0; j < it.n && ok; ++j, ++s) {
+      const int n = uniform(it.n);
+      if (n == 0) continue;
+      for (int j = 0; j < n && ok; ++j) {
+        if (s - ps == NG) products();  // its stage is the next tile's
+        if (!ok) break;
+        if (j == 0 && !wait(&S.a_full[a & 1], a / 2)) break;
         if (!wait(&S.n_full[s % NS], s / NS)) break;
         tc_fence_after();
-        // stage s & 1: the products of tile s - 2, which read it, were issued before
-        const uint32_t ts = tbase + (uint32_t)(s & 1) * 128;
-        const int nt = it.steps(j);
+        const uint32_t ts = tbase + (uint32_t)(s % NG) * 128;
+        const int nt = uniform(it.steps(j));
         const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
-        const uint64_t n1 = desc_at(kmaj, nslot(s));
+        const uint64_t a1 = desc_at(kmaj, abuf(a)), n1 = desc_at(kmaj, nslot(s));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int w = 0; w < 2; ++w)
             tc_mma_f16_by(lead, ts + 64 * w, desc_at(a1, w * C::kA + (ks >> 2) * 16384 + (ks & 3) * 32),
                           desc_at(n1, w * C::kN + (ks >> 2) * 8192 + (ks & 3) * 32), idesc_s, ks > 0);
-        tc_commit_by(lead, smem_u32(&S.s_full[s & 1]));
-        if (j == it.n - 1) tc_commit_by(lead, smem_u32(&S.a_empty[a & 1]));
-        products();
-        pend = true;
-        ps = s;
-        pa = a;
-        pnt = nt;
-        pfirst = j == 0;
-        plast = j == it.n - 1;
+        tc_commit_by(lead, smem_u32(&S.s_full[s % NG]));
+        if (!kDq && j == n - 1) tc_commit_by(lead, smem_u32(&S.a_empty[a & 1]));
+        queue = (queue << 8) | (uint32_t)nt | (j == 0 ? 8u : 0u) | (j == n - 1 ? 16u : 0u);
+        ++s;
       }
       ++a;
     }
-    if (ok) products();
+    while (ok && ps < s) products();
     // every MMA of this CTA has completed before tensor memory is freed
     tc_commit_by(lead, smem_u32(&S.done));
     if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
-  } else if (warp == kWarpAux) {
+  } else if (warp == C::kAux) {
     int s = 0;
     for (; ok && (clean || !kDq) && it.next();) {
       for (int j = 0; j < it.n && ok; ++j, ++s) {
@@ -314,8 +345,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             const bool on = key < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + key] != 0);
             word[c] = __ballot_sync(0xffffffffu, on);
           }
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.n_full[slot]), (uint32_t)((s / NS) & 1)));
-          if (!ok) break;
+          if (!wait(&S.n_full[slot], s / NS)) break;
           const int rows = 16 * it.steps(j);
           unsigned char* k = sm + (nslot(s) - base);
 #pragma unroll
@@ -342,9 +372,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             nl.y = neg_lse2(p.lse_in[g + 1]);
             de.y = p.delta[g + 1];
           }
-          if (s >= NS)
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.n_empty[slot]), (uint32_t)((s / NS - 1) & 1)));
-          if (!ok) break;
+          if (s >= NS && !wait(&S.n_empty[slot], s / NS - 1)) break;
           S.side[slot][lane] = nl;
           S.side[slot][32 + lane] = de;
         }
@@ -352,32 +380,26 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         if (lane == 0) mbar_arrive(smem_u32(&S.n_aux[slot]));
       }
     }
-  } else {
-    const int g = warp >> 2, q4 = warp & 3;
-    const int r = q4 * 32 + lane;  // row of A = TMEM lane
-    const uint32_t trow = tbase + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t ts = trow + (uint32_t)g * 128, tacc = trow + C::kColAcc;
-    const float sc2 = p.scale * kLog2e;
-    const uint64_t sc2x2 = f2_make(sc2, sc2);
-    int a = 0, s = 0;
+  } else if (warp >= C::kEpi) {
+    // ------------------------------------------------------------- epilogue
+    const int q4 = warp & 3, r = q4 * 32 + lane;  // row of A = TMEM lane
+    const uint32_t tacc = tbase + ((uint32_t)(q4 * 32) << 16) + C::kColAcc;
+    int a = 0, last_b = -1;
     bool one = false;
-    auto wait = [&](uint64_t* bar, int phase) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
-      return ok;
-    };
-    for (; ok && it.next();) {
+    for (; ok && it.next(); ) {
       const int row = it.r0 + r;
+      const bool new_b = it.b != last_b;
+      last_b = it.b;
       if (kDq) {
-        // ---------------------------------------------------- dQ and Delta
         const bool valid = row < p.N;
         const size_t grow = (size_t)it.bk * p.N + row;
         const size_t rows = (size_t)p.B * p.H * p.N;
-        if (it.new_b) {
+        if (new_b) {
           one = sees_one(p, it.b, it.len);
-          if (tid == 0) p.alone[it.b] = one;
+          if (r == 0) p.alone[it.b] = one;
         }
         if (it.n == 0) {  // no keys (in this range)
-          if (g == 0 && valid) {
+          if (valid) {
             if (p.nks > 1) {
               p.part_s[it.split * rows + grow] = make_float4(0.f, 0.f, 0.f, 0.f);
             } else {
@@ -388,200 +410,100 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           }
           continue;
         }
-        float nl = -INFINITY;  // rows past the end or without keys: probability zero
-        if (valid) nl = neg_lse2(p.lse_in[grow]);
-        const uint64_t nl2 = f2_make(nl, nl);
-        float c0 = 0.f;
-        uint64_t c2 = 0;
-        bool have_c = false;
-        uint64_t ls = f2_make(0.f, 0.f), ds = f2_make(0.f, 0.f);
-        for (int j = 0; j < it.n; ++j, ++s) {
-          if ((s & 1) != g) continue;
-          if (!wait(&S.s_full[g], s >> 1)) break;
-          if (clean && !wait(&S.n_aux[s % NS], s / NS)) break;
-          tc_fence_after();
-          if (j > 0 && !have_c) {  // the other group has the item's first tile
-            if (!wait(&S.c_full, a)) break;
-            c0 = S.q.c[r];
-            have_c = true;
-          }
-          c2 = f2_make(c0, c0);
-          const int nch = (it.steps(j) + 1) / 2;  // chunks of 32 keys
-#pragma unroll 1
-          for (int c = 0; c < nch; ++c) {
-            uint32_t bits;
-            if (clean) {
-              bits = S.bits[s % NS][c];
-            } else {
-              const int m = it.len - (it.n0 + j) * 64 - 32 * c;
-              bits = m >= 32 ? 0xffffffffu : (1u << m) - 1u;
-            }
-            float x[32], d[32];
-            tmem_ld32(ts + 32 * c, x);
-            tmem_ld32(ts + 64 + 32 * c, d);
-            tmem_wait_ld();
-            if (bits != 0xffffffffu) {
+        const int par = a % C::kSums;
+        if (!wait(&S.x_full[par], a / C::kSums)) break;
+        const float c0 = S.q.c[par][r];
+        float sp = 0.f, sd = 0.f;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (((bits >> i) & 1u) == 0u) {
-                  x[i] = -INFINITY;
-                  d[i] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = f2_split(f2_fma(f2_make(x[2 * i], x[2 * i + 1]), sc2x2, nl2));
-              x[2 * i] = ex2_approx(e.x);
-              x[2 * i + 1] = ex2_approx(e.y);
-            }
-            if (!have_c) {
-              uint64_t w = f2_make(0.f, 0.f), wd = w;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint64_t pp = f2_make(x[2 * i], x[2 * i + 1]);
-                w = f2_add(w, pp);
-                wd = f2_fma(pp, f2_make(d[2 * i], d[2 * i + 1]), wd);
-              }
-              const float2 u = f2_split(w), v = f2_split(wd);
-              const float sw = u.x + u.y;
-              c0 = sw > 1e-30f ? (v.x + v.y) / sw : 0.f;
-              if (!(fabsf(c0) < INFINITY)) c0 = 0.f;  // infinities and NaN of dP take their own way
-              c2 = f2_make(c0, c0);
-              have_c = true;
-              if (a > 0 && !wait(&S.x_read, a - 1)) break;
-              S.q.c[r] = c0;
-              mbar_arrive(smem_u32(&S.c_full));
-            }
-            uint32_t pk[16], dk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t pp = f2_make(x[2 * i], x[2 * i + 1]);
-              const uint64_t t = f2_mul(pp, f2_sub(f2_make(d[2 * i], d[2 * i + 1]), c2));
-              ls = f2_add(ls, pp);
-              ds = f2_add(ds, t);
-              const float2 tt = f2_split(t);
-              pk[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-              dk[i] = pack_bf16(tt.x, tt.y);
-            }
-            tmem_st16u(ts + 16 * c, pk);
-            tmem_st16u(ts + 64 + 16 * c, dk);
-          }
-          if (!ok) break;
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&S.p_full[g]));
+        for (int g = 0; g < NG; ++g) {
+          const float2 x = S.q.sums[par][g][r];
+          sp += x.x;
+          sd += x.y;
         }
-        if (!ok) break;
-        // the row's sums of both groups
-        if (a > 0 && !wait(&S.x_read, a - 1)) break;
-        const float2 l2 = f2_split(ls), d2 = f2_split(ds);
-        S.q.sums[g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
-        mbar_arrive(smem_u32(&S.x_full));
-        if (!wait(&S.x_full, a)) break;
-        const float2 s0 = S.q.sums[0][r], s1 = S.q.sums[1][r];
-        c0 = S.q.c[r];
-        mbar_arrive(smem_u32(&S.x_read));
-        const float sp = s0.x + s1.x, sd = s0.y + s1.y;
+        mbar_arrive(smem_u32(&S.x_read[par]));
         const float delta = fmaf(c0, sp, sd), f = c0 - delta;
+        if (valid) {
+          if (p.nks > 1) p.part_s[it.split * rows + grow] = make_float4(c0, sp, sd, 1.f);
+          else p.delta[grow] = delta;
+        }
         if (!wait(&S.acc_full, a)) break;
-        ++a;
         tc_fence_after();
-        const float out = one ? 0.f : p.scale;
+        unsigned char* stage = sm + (abuf(a) - base);  // A1, which no MMA reads any more
 #pragma unroll 1
-        for (int c = g * (D / 2); c < (g + 1) * (D / 2); c += 32) {
-          float x[32], y[32];
-          tmem_ld32(tacc + c, x);
-          tmem_ld32(tacc + D + c, y);
+        for (int c = 0; c < D; c += 16) {
+          float x[16], y[16];
+          tmem_ld16(tacc + c, x);
+          tmem_ld16(tacc + D + c, y);
           tmem_wait_ld();
-          if (!valid) continue;
           if (p.nks > 1) {
             const size_t at = (it.split * rows + grow) * D + c;
+            if (valid) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              *reinterpret_cast<float4*>(p.part_dq + at + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-              *reinterpret_cast<float4*>(p.part_dqb + at + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              for (int i = 0; i < 16; i += 4) {
+                *reinterpret_cast<float4*>(p.part_dq + at + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                *reinterpret_cast<float4*>(p.part_dqb + at + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              }
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<bf16*>(p.dq) + grow * D + c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = one ? 0.f : fmaf(f, y[i], x[i]) * out;
+            for (int i = 0; i < 16; ++i) x[i] = one ? 0.f : fmaf(f, y[i], x[i]) * p.scale;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                  pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+            for (int i = 0; i < 2; ++i) {
+              const int cc = c / 8 + i;
+              *reinterpret_cast<uint4*>(stage + (cc >> 3) * 16384 + sw128(r, cc & 7)) =
+                  make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                             pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+            }
           }
         }
         tc_fence_before();
         mbar_arrive(smem_u32(&S.acc_free));
-        if (g == 0 && valid) {
-          if (p.nks > 1) p.part_s[it.split * rows + grow] = make_float4(c0, sp, sd, 1.f);
-          else p.delta[grow] = delta;
+        fence_proxy_async_smem();  // generic writes -> TMA store
+        mbar_arrive(smem_u32(&S.staged));
+        if (q4 == 0) {
+          if (!wait(&S.staged, a)) break;
+          if (lane == 0) {
+            if (p.nks == 1) {
+#pragma unroll
+              for (int h = 0; h < H; ++h) tma_store_3d(&tdq, 64 * h, it.r0, it.bk, abuf(a) + h * 16384);
+              bulk_commit_group();
+              bulk_wait_read_all();
+            }
+            mbar_arrive(smem_u32(&S.a_empty[a & 1]));
+          }
         }
+        ++a;
       } else {
-        // ------------------------------------------------------- dK and dV
         // keys that are not seen: whatever their rows hold, it stays in them
         const bool seen = row < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + row] != 0);
-        bf16* dst = static_cast<bf16*>(g == 0 ? p.dv : p.dk) + ((size_t)it.bk * p.S + row) * D;
+        const size_t at = ((size_t)it.bk * p.S + row) * D;
         if (it.n == 0) {
           if (p.nz == 1 && row < p.S)
-            for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 8; ++c) {
+              reinterpret_cast<uint4*>(static_cast<bf16*>(p.dk) + at)[c] = make_uint4(0, 0, 0, 0);
+              reinterpret_cast<uint4*>(static_cast<bf16*>(p.dv) + at)[c] = make_uint4(0, 0, 0, 0);
+            }
           continue;
         }
-        for (int j = 0; j < it.n; ++j, ++s) {
-          if ((s & 1) != g) continue;
-          if (!wait(&S.n_aux[s % NS], s / NS)) break;
-          if (!wait(&S.s_full[g], s >> 1)) break;
-          tc_fence_after();
-          const float2* side = S.side[s % NS];
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float x[32], d[32];
-            tmem_ld32(ts + 32 * c, x);
-            tmem_ld32(ts + 64 + 32 * c, d);
-            tmem_wait_ld();
-            uint32_t pk[16], dk[16];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float4 nl = *reinterpret_cast<const float4*>(side + 16 * c + i);
-              const float4 de = *reinterpret_cast<const float4*>(side + 32 + 16 * c + i);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int e = 2 * (i + u);
-                const float2 t = f2_split(f2_fma(f2_make(x[e], x[e + 1]), sc2x2,
-                                                 u ? f2_make(nl.z, nl.w) : f2_make(nl.x, nl.y)));
-                const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
-                const float2 q = f2_split(f2_mul(f2_make(p0, p1), f2_sub(f2_make(d[e], d[e + 1]),
-                                                                         u ? f2_make(de.z, de.w) : f2_make(de.x, de.y))));
-                pk[i + u] = pack_bf16(p0, p1);
-                dk[i + u] = pack_bf16(q.x, q.y);
-              }
-            }
-            tmem_st16u(ts + 16 * c, pk);
-            tmem_st16u(ts + 64 + 16 * c, dk);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&S.p_full[g]));
-        }
-        if (!ok) break;
+        const float fk = p.alone[it.b] != 0 ? 0.f : p.scale;
         if (!wait(&S.acc_full, a)) break;
         ++a;
         tc_fence_after();
-        const float f = g == 0 ? 1.f : (p.alone[it.b] != 0 ? 0.f : p.scale);
-        const uint32_t tsrc = tacc + (g == 0 ? D : 0);
-        float* part = g == 0 ? p.part_dv : p.part_dk;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < 2 * D; c += 32) {  // accA is dK, accB dV
           float x[32];
-          tmem_ld32(tsrc + c, x);
+          tmem_ld32(tacc + c, x);
           tmem_wait_ld();
           if (row >= p.S) continue;
+          const bool is_k = c < D;
           if (p.nz > 1) {
-            float4* to = reinterpret_cast<float4*>(part + (((size_t)it.i * p.nz + it.slot) * 128 + r) * D + c);
+            float4* to = reinterpret_cast<float4*>((is_k ? p.part_dk : p.part_dv) +
+                                                   (((size_t)it.i * p.nz + it.slot) * 128 + r) * D + c % D);
 #pragma unroll
             for (int i = 0; i < 8; ++i) to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           } else {
-            uint4* to = reinterpret_cast<uint4*>(dst + c);
+            uint4* to = reinterpret_cast<uint4*>(static_cast<bf16*>(is_k ? p.dk : p.dv) + at + c % D);
+            const float f = is_k ? fk : 1.f;
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = seen && f != 0.f ? x[i] * f : 0.f;
 #pragma unroll
@@ -594,12 +516,169 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         mbar_arrive(smem_u32(&S.acc_free));
       }
     }
+    if (kDq && r == 0) bulk_wait_all();
+  } else {
+    // ----------------------------------------------------------- P and dS
+    const int g = warp >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t ts = tbase + ((uint32_t)(q4 * 32) << 16) + (uint32_t)g * 128;
+    const float sc2 = p.scale * kLog2e;
+    const uint64_t sc2x2 = f2_make(sc2, sc2);
+    int a = 0, s = 0;
+    float lse_next = 0.f;
+    if (kDq) lse_next = p.lse_in[it.peek(r)];
+    for (; ok && it.next();) {
+      if (kDq) {
+        const float lse = lse_next;
+        lse_next = p.lse_in[it.peek(r)];
+        if (it.n == 0) continue;
+        const int par = a % C::kSums;
+        const float nl = it.r0 + r < p.N ? neg_lse2(lse) : -INFINITY;  // rows past the end: probability zero
+        const uint64_t nl2 = f2_make(nl, nl);
+        bool have_c = false;
+        uint64_t c2 = 0, ls = 0, ds = 0;
+        for (int j = 0; j < it.n; ++j, ++s) {
+          if (s % NG != g) continue;
+          if (!wait(&S.s_full[g], s / NG)) break;
+          if (clean && !wait(&S.n_aux[s % NS], s / NS)) break;
+          tc_fence_after();
+          if (!have_c && j > 0) {  // another group has the item's first tile
+            if (!wait(&S.c_full[par], a / C::kSums)) break;
+            const float c0 = S.q.c[par][r];
+            c2 = f2_make(c0, c0);
+            have_c = true;
+          }
+          const int left = it.len - (it.n0 + j) * 64;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            const int m = left - 32 * c;
+            if (m <= 0) break;
+            uint32_t bits = m >= 32 ? 0xffffffffu : (1u << m) - 1u;
+            if (clean) bits = S.bits[s % NS][c];
+            if (!have_c) {
+              float d[32];
+              tmem_ld32(ts + 64, d);
+              tmem_wait_ld();
+              if (bits != 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (((bits >> i) & 1u) == 0u) d[i] = 0.f;
+              }
+              uint64_t t = f2_make(d[0], d[1]);
+#pragma unroll
+              for (int i = 2; i < 32; i += 2) t = f2_add(t, f2_make(d[i], d[i + 1]));
+              const float2 u = f2_split(t);
+              const float c0 = (u.x + u.y) * (1.f / (float)max(1, __popc(bits)));
+              c2 = f2_make(c0, c0);
+              have_c = true;
+              if (a >= C::kSums && !wait(&S.x_read[par], a / C::kSums - 1)) break;
+              S.q.c[par][r] = c0;
+              mbar_arrive(smem_u32(&S.c_full[par]));
+            }
+            float x[32];
+            uint32_t pk[16];
+            tmem_ld32(ts + 32 * c, x);
+            tmem_wait_ld();
+            if (bits != 0xffffffffu) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (((bits >> i) & 1u) == 0u) x[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = f2_split(f2_fma(f2_make(x[2 * i], x[2 * i + 1]), sc2x2, nl2));
+              x[2 * i] = ex2_approx(e.x);
+              x[2 * i + 1] = ex2_approx(e.y);
+              ls = f2_add(ls, f2_make(x[2 * i], x[2 * i + 1]));
+              pk[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            }
+            tmem_st16u(ts + 16 * c, pk);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float d[16];
+              tmem_ld16(ts + 64 + 32 * c + 16 * h, d);
+              tmem_wait_ld();
+              if (bits != 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (((bits >> (16 * h + i)) & 1u) == 0u) d[i] = 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint64_t t = f2_mul(f2_make(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]),
+                                          f2_sub(f2_make(d[2 * i], d[2 * i + 1]), c2));
+                ds = f2_add(ds, t);
+                const float2 tt = f2_split(t);
+                pk[8 * h + i] = pack_bf16(tt.x, tt.y);
+              }
+            }
+            tmem_st16u(ts + 64 + 16 * c, pk);
+          }
+          if (!ok) break;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&S.p_full[g]));
+        }
+        if (!ok) break;
+        if (a >= C::kSums && !wait(&S.x_read[par], a / C::kSums - 1)) break;
+        const float2 l2 = f2_split(ls), d2 = f2_split(ds);
+        S.q.sums[par][g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
+        mbar_arrive(smem_u32(&S.x_full[par]));
+        ++a;
+      } else {
+        for (int j = 0; j < it.n; ++j, ++s) {
+          if (s % NG != g) continue;
+          if (!wait(&S.n_aux[s % NS], s / NS)) break;
+          if (!wait(&S.s_full[g], s / NG)) break;
+          tc_fence_after();
+          const float2* side = S.side[s % NS];
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float x[32], d[32];
+            tmem_ld32(ts + 32 * c, x);
+            tmem_ld32(ts + 64 + 32 * c, d);
+            tmem_wait_ld();
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 nl = *reinterpret_cast<const float4*>(side + 16 * c + i);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int e = 2 * (i + u);
+                const float2 t = f2_split(f2_fma(f2_make(x[e], x[e + 1]), sc2x2,
+                                                 u ? f2_make(nl.z, nl.w) : f2_make(nl.x, nl.y)));
+                x[e] = ex2_approx(t.x);
+                x[e + 1] = ex2_approx(t.y);
+                pk[i + u] = pack_bf16(x[e], x[e + 1]);
+              }
+            }
+            tmem_st16u(ts + 16 * c, pk);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 de = *reinterpret_cast<const float4*>(side + 32 + 16 * c + i);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int e = 2 * (i + u);
+                const float2 q = f2_split(f2_mul(f2_make(x[e], x[e + 1]),
+                                                 f2_sub(f2_make(d[e], d[e + 1]),
+                                                        u ? f2_make(de.z, de.w) : f2_make(de.x, de.y))));
+                pk[i + u] = pack_bf16(q.x, q.y);
+              }
+            }
+            tmem_st16u(ts + 64 + 16 * c, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&S.p_full[g]));
+        }
+      }
+    }
   }
 
   if (!ok) report_status(p.status, LLSA_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == C::kMma) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -674,13 +753,14 @@ cross_dkv_join(CrossParams p, int grid) {
 }
 
 template <int D, bool kDq>
-cudaError_t launch_pass(const CrossParams& p, const CUtensorMap* a, const CUtensorMap* n, int grid, cudaStream_t s) {
-  constexpr size_t smem = Cfg<D>::kEnd + sizeof(Shared<Cfg<D>::kSlots>);
+cudaError_t launch_pass(const CrossParams& p, const CUtensorMap* a, const CUtensorMap* n, const CUtensorMap& dq,
+                        int grid, cudaStream_t s) {
+  constexpr size_t smem = Cfg<D>::kEnd + sizeof(Shared<Cfg<D>>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   cudaError_t e =
       cudaFuncSetAttribute(cross_bwd_tc_kernel<D, kDq>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cross_bwd_tc_kernel<D, kDq><<<grid, kThreads, smem, s>>>(a[0], a[1], n[0], n[1], p);
+  cross_bwd_tc_kernel<D, kDq><<<grid, Cfg<D>::kThreads, smem, s>>>(a[0], a[1], n[0], n[1], dq, p);
   return cudaGetLastError();
 }
 
@@ -689,7 +769,7 @@ cudaError_t launch_typed(const CrossParams& p, const CUtensorMap* q128, const CU
                          const CUtensorMap* kv128, const CUtensorMap* q64, cudaStream_t s) {
   const long long items = (long long)p.B * p.H * p.nks * ((p.N + 127) / 128);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = launch_pass<D, true>(p, q128, kv64, (int)(items < kCrossSms ? items : kCrossSms), s);
+  cudaError_t e = launch_pass<D, true>(p, q128, kv64, q128[2], (int)(items < kCrossSms ? items : kCrossSms), s);
   const size_t rows = (size_t)p.B * p.H * p.N;
   if (e == cudaSuccess && p.nks > 1) {
     cross_dq_join<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
@@ -697,7 +777,7 @@ cudaError_t launch_typed(const CrossParams& p, const CUtensorMap* q128, const CU
   }
   if (e != cudaSuccess || p.S == 0) return e;
   const int grid = CrossPairs::grid_of((long long)p.B * p.H, p.N, p.S, p.nz);
-  e = launch_pass<D, false>(p, kv128, q64, grid, s);
+  e = launch_pass<D, false>(p, kv128, q64, q128[2], grid, s);
   if (e == cudaSuccess && p.nz > 1) {
     const size_t threads = (size_t)p.B * p.H * p.S * (D / 4);
     cross_dkv_join<D><<<dim3((unsigned)((threads + 255) / 256), 2), 256, 0, s>>>(p, grid);

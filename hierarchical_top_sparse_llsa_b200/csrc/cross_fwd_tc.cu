@@ -68,7 +68,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Shared& S = *reinterpret_cast<Shared*>(sm + C::kEnd);
   const uint32_t base = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const bool clean = p.mask != nullptr || p.kv_len != nullptr;
   bool ok = true;
 
@@ -97,7 +97,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = S.tmem_base;
+  const uint32_t tbase = uniform(S.tmem_base);
   auto qslot = [&](int t) { return base + (uint32_t)(t % C::kQ) * C::kTile; };
   auto kvslot = [&](int f) { return base + (uint32_t)(C::kQ + f % C::kKv) * C::kTile; };
   CrossItems it(p, items, C::kKv / 2);
@@ -169,16 +169,18 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       if (plast) tc_commit_by(lead, smem_u32(&S.o_full[w]));
     };
     for (; ok && it.next();) {
-      if (it.nkt == 0) continue;
-      if (!it.resident || it.new_run) {
+      const int nkt = uniform(it.nkt);
+      if (nkt == 0) continue;
+      const bool resident = nkt <= it.cap;
+      if (!resident || it.new_run) {
         frun = f;
-        f += 2 * it.nkt;
+        f += 2 * nkt;
       }
       const int t0 = t;
       t += it.act1 ? 2 : 1;
-      for (int j = 0; j < it.nkt && ok; ++j) {
+      for (int j = 0; j < nkt && ok; ++j) {
         const int fk = frun + 2 * j;
-        const int nt = it.steps(j);
+        const int nt = uniform(it.steps(j));
         const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
         const uint64_t k = desc_at(kmaj, kvslot(fk));
         if (!wait(&S.kv_full[fk % C::kKv], fk / C::kKv)) break;
@@ -202,8 +204,8 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         pf = fk + 1;
         pnt = nt;
         pfirst = j == 0;
-        plast = j == it.nkt - 1;
-        pfree = !it.resident || it.last_of_run;
+        plast = j == nkt - 1;
+        pfree = !resident || it.last_of_run;
         if (pfree) tc_commit_by(lead, smem_u32(&S.kv_empty[fk % C::kKv]));
       }
     }

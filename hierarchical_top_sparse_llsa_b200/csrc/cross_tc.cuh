@@ -14,6 +14,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // with 128-byte swizzle (the TMA layout of every tile here).
 __device__ __forceinline__ uint32_t sw128(int r, int jj) { return (uint32_t)(r * 128 + ((jj ^ (r & 7)) << 4)); }
 
+// A value that is the same in all lanes, where the compiler sees that it is:
+// the operands of the MMAs and TMA copies then stay in uniform registers.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Descriptor of an operand tile at shared address a, given that of address 0
 // (addresses stay below 2^18, so the field takes the sum).
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc0, uint32_t a) { return desc0 + (a >> 4); }
