@@ -7,6 +7,18 @@
 
 namespace llsa {
 
+// n items cut into one run per CTA, the first n % grid of them longer by one.
+struct CrossRuns {
+  int64_t each, more;
+  __host__ __device__ __forceinline__ int64_t begin(int c) const { return each * c + (c < more ? c : more); }
+  __host__ __device__ __forceinline__ int cta_of(int64_t x) const {
+    const int64_t longer = more * (each + 1);
+    return (int)(x < longer ? x / (each + 1) : more + (x - longer) / each);
+  }
+};
+inline CrossRuns cross_runs(int64_t n, int grid) { return {n / grid, n % grid}; }
+inline int64_t cross_tiles(int64_t n, int t) { return (n + t - 1) / t; }
+
 struct CrossParams {
   const void* q;
   const void* k;
@@ -40,6 +52,7 @@ struct CrossParams {
   int S, D;
   int nks;         // splits of the keys (fwd: of O; bwd: of dQ)
   int nz;          // bwd: segments of the query tiles (dK, dV)
+  CrossRuns runs;  // bf16: what each CTA does
   float scale;
 };
 
@@ -60,35 +73,6 @@ CrossPlan cross_tc_fwd_plan(long long BH, int N, int S);
 CrossPlan cross_tc_bwd_plan(long long BH, int N, int S);
 
 constexpr int kCrossSms = 148;  // SMs of a B200
-
-// The second pass of the bf16 backward walks pairs of a key tile (128) and a
-// tile of 64 query rows, the queries innermost; CTA c takes the pairs from
-// begin(c) to begin(c + 1).  A key tile that several CTAs share has up to
-// slots() parts.  Whole key tiles are given out (no parts) where there are
-// many of them, at least four a CTA, or nothing to cut.
-struct CrossPairs {
-  long long nq, total;  // query tiles of a head; all pairs
-  int grid;
-  bool whole;
-  __host__ __device__ __forceinline__ static long long tiles(long long n, int t) { return (n + t - 1) / t; }
-  __host__ __device__ __forceinline__ CrossPairs(long long BH, int N, int S, int nz, int grid_)
-      : nq(tiles(N, 64)), total(BH * tiles(S, 128) * nq), grid(grid_), whole(nz == 1) {}
-  __host__ __device__ __forceinline__ long long begin(int c) const {
-    return whole ? total / nq * c / grid * nq : total * c / grid;
-  }
-  // the CTA that has pair x (parts only)
-  __host__ __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * grid - 1) / total); }
-  static int slots(long long BH, int N, int S) {
-    const long long nq = tiles(N, 64), units = BH * tiles(S, 128), total = units * nq;
-    if (total == 0 || nq == 1 || units >= 4 * kCrossSms || units % kCrossSms == 0) return 1;
-    // an interval of nq pairs meets at most ceil((nq - 1) / (total / grid)) + 1 CTAs
-    return (int)(tiles(total < kCrossSms ? total : kCrossSms, (int)units) + 1);
-  }
-  static int grid_of(long long BH, int N, int S, int nz) {
-    const long long units = BH * tiles(S, 128), n = nz == 1 ? units : units * tiles(N, 64);
-    return (int)(n < kCrossSms ? n : kCrossSms);
-  }
-};
 
 // maps: Q, K, V, O as 3D [B H, rows, D] bf16, box 128 rows x 64 columns, 128-byte swizzle
 cudaError_t launch_cross_fwd_tc(const CrossParams& p, const CUtensorMap* maps, cudaStream_t s);

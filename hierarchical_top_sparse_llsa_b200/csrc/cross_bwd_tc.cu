@@ -80,35 +80,33 @@ struct Shared {
 };
 
 // The items of a CTA, in order.  First pass: 128 query rows against one range
-// of the keys.  Second pass: 128 keys against one range of the queries, cut
-// from the CTA's share of all pairs.
+// of the keys.  Second pass: 128 keys (a key tile) against one range of the
+// queries.  There the CTA's run is of pairs of a key tile and a tile of 64
+// queries, the queries innermost, or of key tiles (nz == 1).
 template <bool kDq>
 struct BwdItems {
   const CrossParams& p;
-  CrossPairs w;                // second pass
-  int i, end, nt;              // kDq: items; else units (key tiles); nt: row tiles per head
-  long long beg, fin;          // second pass: the CTA's pairs
-  int bk, b, split, slot, tile, r0, len;
+  int i, end, nt, nq;          // kDq: items; else key tiles; nt: row tiles per head; nq: query tiles of a head
+  int64_t beg, fin;            // second pass: the CTA's pairs
+  int bk, b, split, tile, r0, len;
   int n0, n;                   // first tile of 64 streamed rows, how many
 
-  __device__ __forceinline__ BwdItems(const CrossParams& p_)
-      : p(p_), w((long long)p_.B * p_.H, p_.N, p_.S, p_.nz, (int)gridDim.x), b(-1) {
-    if (kDq) {
-      nt = (p.N + 127) / 128;
-      const long long items = (long long)p.B * p.H * p.nks * nt;
-      i = (int)(items * blockIdx.x / gridDim.x) - 1;
-      end = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  __device__ __forceinline__ BwdItems(const CrossParams& p_) : p(p_), b(-1) {
+    beg = p.runs.begin(blockIdx.x);
+    fin = p.runs.begin(blockIdx.x + 1);
+    nq = (p.N + 63) / 64;
+    nt = ((kDq ? p.N : p.S) + 127) / 128;
+    if (!kDq && p.nz > 1) {
+      i = (int)(beg / nq) - 1;
+      end = (int)((fin + nq - 1) / nq);
     } else {
-      nt = (p.S + 127) / 128;
-      beg = w.begin(blockIdx.x);
-      fin = w.begin(blockIdx.x + 1);
-      i = (int)(beg / w.nq) - 1;
-      end = (int)((fin + w.nq - 1) / w.nq);
+      i = (int)beg - 1;
+      end = (int)fin;
     }
     const int run = (i + 1) / nt;
     tile = i - run * nt;  // of the item before the first
-    split = kDq ? run % p.nks : 0;
     bk = kDq ? run / p.nks : run;
+    split = kDq ? run - bk * p.nks : 0;
     range();
   }
   // what the head and the range of the keys settle
@@ -120,9 +118,13 @@ struct BwdItems {
       len = cross_len(p, b);
     }
     if (kDq) {
-      const int kt = (len + 63) / 64;
-      n0 = p.nks == 1 ? 0 : (int)((long long)kt * split / p.nks);
-      n = (p.nks == 1 ? kt : (int)((long long)kt * (split + 1) / p.nks)) - n0;
+      n0 = 0;
+      n = (len + 63) / 64;
+      if (p.nks > 1) {  // the first n % nks ranges are longer by one
+        const int each = n / p.nks, more = n - each * p.nks;
+        n0 = each * split + min(split, more);
+        n = each + (split < more);
+      }
     }
   }
   __device__ __forceinline__ bool next() {
@@ -137,10 +139,14 @@ struct BwdItems {
     }
     r0 = tile * 128;
     if (!kDq) {
-      const long long u = (long long)i * w.nq;
-      n0 = (int)(beg > u ? beg - u : 0);
-      n = (int)(fin < u + w.nq ? fin - u : w.nq) - n0;
-      slot = p.nz > 1 ? (int)blockIdx.x - w.cta_of(u) : 0;
+      n0 = 0;
+      n = nq;
+      if (p.nz > 1) {
+        const int64_t u = (int64_t)i * nq;
+        if (beg > u) n0 = (int)(beg - u);
+        if (fin < u + nq) n = (int)(fin - u);
+        n -= n0;
+      }
       if (r0 >= len) n = 0;  // no key of the tile is seen
     }
     return true;
@@ -232,7 +238,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
   auto abuf = [&](int a) { return base + (uint32_t)(a & 1) * 2 * C::kA; };
   auto nslot = [&](int s) { return base + C::kOffN + (uint32_t)(s % NS) * 2 * C::kN; };
   auto wait = [&](uint64_t* bar, int phase) {  // by whole warps
-    return ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
+    return ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), (uint32_t)(phase & 1)));
   };
   BwdItems<kDq> it(p);
 
@@ -242,7 +248,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       for (; ok && it.next();) {
         if (it.n == 0) continue;
         uint64_t* full = &S.a_full[a & 1];
-        if (a >= 2) ok = mbar_wait_bounded(smem_u32(&S.a_empty[a & 1]), (uint32_t)((a / 2 - 1) & 1));
+        if (a >= 2) ok = mbar_wait(smem_u32(&S.a_empty[a & 1]), (uint32_t)((a / 2 - 1) & 1));
         if (!ok) break;
         mbar_arrive_expect_tx(smem_u32(full), 2 * C::kA);
 #pragma unroll
@@ -252,7 +258,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         }
         ++a;
         for (int j = 0; j < it.n; ++j, ++s) {
-          if (s >= NS) ok = mbar_wait_bounded(smem_u32(&S.n_empty[s % NS]), (uint32_t)((s / NS - 1) & 1));
+          if (s >= NS) ok = mbar_wait(smem_u32(&S.n_empty[s % NS]), (uint32_t)((s / NS - 1) & 1));
           if (!ok) break;
           full = &S.n_full[s % NS];
           mbar_arrive_expect_tx(smem_u32(full), 2 * C::kN);
@@ -265,9 +271,9 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       }
       // no copy may still be landing when the CTA exits
       for (int i = a > 2 ? a - 2 : 0; i < a; ++i)
-        if (!mbar_wait_bounded(smem_u32(&S.a_full[i & 1]), (uint32_t)((i / 2) & 1))) ok = false;
+        if (!mbar_wait(smem_u32(&S.a_full[i & 1]), (uint32_t)((i / 2) & 1))) ok = false;
       for (int i = s > NS ? s - NS : 0; i < s; ++i)
-        if (!mbar_wait_bounded(smem_u32(&S.n_full[i % NS]), (uint32_t)((i / NS) & 1))) ok = false;
+        if (!mbar_wait(smem_u32(&S.n_full[i % NS]), (uint32_t)((i / NS) & 1))) ok = false;
     }
   } else if (warp == C::kMma) {
     // the whole warp walks; one lane issues
@@ -331,7 +337,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     while (ok && ps < s) products();
     // every MMA of this CTA has completed before tensor memory is freed
     tc_commit_by(lead, smem_u32(&S.done));
-    if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
+    if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
   } else if (warp == C::kAux) {
     int s = 0;
     for (; ok && (clean || !kDq) && it.next();) {
@@ -486,6 +492,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           continue;
         }
         const float fk = p.alone[it.b] != 0 ? 0.f : p.scale;
+        size_t part_row = 0;  // of the parts
+        if (p.nz > 1) {
+          const int slot = (int)blockIdx.x - p.runs.cta_of((int64_t)it.i * it.nq);
+          part_row = ((size_t)it.i * p.nz + slot) * 128 + r;
+        }
         if (!wait(&S.acc_full, a)) break;
         ++a;
         tc_fence_after();
@@ -498,7 +509,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           const bool is_k = c < D;
           if (p.nz > 1) {
             float4* to = reinterpret_cast<float4*>((is_k ? p.part_dk : p.part_dv) +
-                                                   (((size_t)it.i * p.nz + it.slot) * 128 + r) * D + c % D);
+                                                   part_row * D + c % D);
 #pragma unroll
             for (int i = 0; i < 8; ++i) to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           } else {
@@ -720,7 +731,7 @@ cross_dq_join(CrossParams p) {
 // tensor (blockIdx.y: dV, dK).
 template <int D>
 __global__ void __launch_bounds__(256)
-cross_dkv_join(CrossParams p, int grid) {
+cross_dkv_join(CrossParams p) {
   constexpr int T = D / 4;
   const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
   const size_t krow = at / T;
@@ -731,9 +742,9 @@ cross_dkv_join(CrossParams p, int grid) {
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (key < cross_len(p, b) && (p.mask == nullptr || p.mask[(size_t)b * p.S + key] != 0) &&
       !(is_k && p.alone[b] != 0)) {
-    const CrossPairs w((long long)p.B * p.H, p.N, p.S, p.nz, grid);
-    const long long u = (long long)bk * ((p.S + 127) / 128) + key / 128;
-    const int n = w.cta_of(u * w.nq + w.nq - 1) - w.cta_of(u * w.nq) + 1;
+    const int nq = (p.N + 63) / 64;
+    const int64_t u = (int64_t)bk * ((p.S + 127) / 128) + key / 128;
+    const int n = p.runs.cta_of(u * nq + nq - 1) - p.runs.cta_of(u * nq) + 1;
     const float* src = (is_k ? p.part_dk : p.part_dv) + ((size_t)u * p.nz * 128 + key % 128) * D + c;
     for (int z = 0; z < n; ++z) {
       const float4 x = *reinterpret_cast<const float4*>(src + (size_t)z * 128 * D);
@@ -765,34 +776,50 @@ cudaError_t launch_pass(const CrossParams& p, const CUtensorMap* a, const CUtens
 }
 
 template <int D>
-cudaError_t launch_typed(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,
-                         const CUtensorMap* kv128, const CUtensorMap* q64, cudaStream_t s) {
-  const long long items = (long long)p.B * p.H * p.nks * ((p.N + 127) / 128);
+cudaError_t launch_typed(CrossParams p, const CUtensorMap* q128, const CUtensorMap* kv64, const CUtensorMap* kv128,
+                         const CUtensorMap* q64, cudaStream_t s) {
+  const int64_t items = (int64_t)p.B * p.H * p.nks * cross_tiles(p.N, 128);
+  int grid = (int)(items < kCrossSms ? items : kCrossSms);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = launch_pass<D, true>(p, q128, kv64, q128[2], (int)(items < kCrossSms ? items : kCrossSms), s);
+  p.runs = cross_runs(items, grid);
+  cudaError_t e = launch_pass<D, true>(p, q128, kv64, q128[2], grid, s);
   const size_t rows = (size_t)p.B * p.H * p.N;
   if (e == cudaSuccess && p.nks > 1) {
     cross_dq_join<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || p.S == 0) return e;
-  const int grid = CrossPairs::grid_of((long long)p.B * p.H, p.N, p.S, p.nz);
+  const int64_t pairs = (int64_t)p.B * p.H * cross_tiles(p.S, 128) * (p.nz > 1 ? cross_tiles(p.N, 64) : 1);
+  grid = (int)(pairs < kCrossSms ? pairs : kCrossSms);
+  p.runs = cross_runs(pairs, grid);
   e = launch_pass<D, false>(p, kv128, q64, q128[2], grid, s);
   if (e == cudaSuccess && p.nz > 1) {
     const size_t threads = (size_t)p.B * p.H * p.S * (D / 4);
-    cross_dkv_join<D><<<dim3((unsigned)((threads + 255) / 256), 2), 256, 0, s>>>(p, grid);
+    cross_dkv_join<D><<<dim3((unsigned)((threads + 255) / 256), 2), 256, 0, s>>>(p);
     e = cudaGetLastError();
   }
   return e;
 }
 
+// Parts of a key tile: as many as its query tiles' pairs meet CTAs.  Whole key
+// tiles are given out where there are many of them, at least four a CTA, or
+// nothing to cut.
+int parts_of_key_tile(int64_t BH, int N, int S) {
+  const int64_t nq = cross_tiles(N, 64), units = BH * cross_tiles(S, 128), total = units * nq;
+  if (total == 0 || nq == 1 || units >= 4 * kCrossSms || units % kCrossSms == 0) return 1;
+  // a run has at least floor(total / grid) pairs, and an interval of nq pairs
+  // meets at most ceil((nq - 1) / that) + 1 runs
+  const int64_t grid = total < kCrossSms ? total : kCrossSms;
+  return (int)(cross_tiles(nq - 1, (int)(total / grid > nq ? nq : total / grid)) + 1);
+}
+
 }  // namespace
 
 CrossPlan cross_tc_bwd_plan(long long BH, int N, int S) {
-  const long long units = BH * (((long long)N + 127) / 128), kt = ((long long)S + 63) / 64;
-  long long nks = kCrossSms / units;
+  const int64_t units = BH * cross_tiles(N, 128), kt = cross_tiles(S, 64);
+  int64_t nks = kCrossSms / units;
   if (nks > kt) nks = kt;
-  return {nks < 1 ? 1 : (int)nks, CrossPairs::slots(BH, N, S)};
+  return {nks < 1 ? 1 : (int)nks, parts_of_key_tile(BH, N, S)};
 }
 
 cudaError_t launch_cross_bwd_tc(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,

@@ -56,11 +56,79 @@ struct Shared {
   uint32_t tmem_base;
 };
 
+// The items of a CTA, in order: 256 query rows of one key head against one
+// range of its key tiles.  Every warp role walks them by itself; rows are
+// innermost, so items of the same keys follow one another (a run).
+struct FwdItems {
+  const CrossParams& p;
+  int i, end, nt, cap;
+  int R;                       // query rows of a key head
+  size_t rows;                 // and of all of them
+  int bk, b, split, tile, r0, len;  // the item: key head, batch entry, key range, rows, keys seen at the front
+  int kt0, nkt;                // its key tiles
+  bool act1;                   // whether its second tile of 128 rows has any
+  bool first, new_run, last_of_run;
+  bool resident;               // its key tiles fit in the ring: loaded once for the run
+
+  __device__ __forceinline__ FwdItems(const CrossParams& p_, int cap_) : p(p_), cap(cap_), b(-1) {
+    R = p.N;
+    rows = (size_t)p.B * p.H * R;
+    nt = (R + 255) / 256;
+    i = (int)p.runs.begin(blockIdx.x) - 1;
+    end = (int)p.runs.begin(blockIdx.x + 1);
+    const int run = (i + 1) / nt;
+    tile = i - run * nt;  // of the item before the first
+    bk = run / p.nks;
+    split = run - bk * p.nks;
+    range();
+    first = true;
+  }
+  __device__ __forceinline__ void range() {
+    const int nb = bk / p.H;
+    if (nb >= p.B) return;  // past the last item
+    if (nb != b) {
+      b = nb;
+      len = cross_len(p, b);
+    }
+    kt0 = 0;
+    nkt = (len + 127) / 128;
+    if (p.nks > 1) {  // the first nkt % nks ranges are longer by one
+      const int each = nkt / p.nks, more = nkt - each * p.nks;
+      kt0 = each * split + min(split, more);
+      nkt = each + (split < more);
+    }
+    resident = nkt <= cap;
+  }
+  __device__ __forceinline__ bool next() {
+    if (i + 1 >= end) return false;
+    new_run = first;
+    first = false;
+    ++i;
+    if (++tile == nt) {
+      tile = 0;
+      new_run = true;
+      if (++split == p.nks) {
+        split = 0;
+        ++bk;
+      }
+      range();
+    }
+    last_of_run = tile == nt - 1 || i + 1 == end;
+    r0 = tile * 256;
+    act1 = r0 + 128 < R;
+    return true;
+  }
+  // 16-key steps of key tile j of the item
+  __device__ __forceinline__ int steps(int j) const {
+    const int n = len - (kt0 + j) * 128;
+    return n >= 128 ? 8 : (n + 15) >> 4;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, CrossParams p,
-                    int items) {
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, CrossParams p) {
   using C = Cfg<D>;
   constexpr int H = D / 64;  // 64-column halves of a tile
   extern __shared__ unsigned char smem_raw[];
@@ -100,7 +168,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
   const uint32_t tbase = uniform(S.tmem_base);
   auto qslot = [&](int t) { return base + (uint32_t)(t % C::kQ) * C::kTile; };
   auto kvslot = [&](int f) { return base + (uint32_t)(C::kQ + f % C::kKv) * C::kTile; };
-  CrossItems it(p, items, C::kKv / 2);
+  FwdItems it(p, C::kKv / 2);
 
   if (warp == kWarpLoad) {
     if (lane == 0) {
@@ -111,7 +179,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int h = 0; h < H; ++h) tma_load_3d(dst + h * 16384, map, 64 * h, row, bk, smem_u32(bar));
       };
       auto load_q = [&](int w) {
-        if (t >= C::kQ) ok = mbar_wait_bounded(smem_u32(&S.q_empty[t % C::kQ]), (uint32_t)((t / C::kQ - 1) & 1));
+        if (t >= C::kQ) ok = mbar_wait(smem_u32(&S.q_empty[t % C::kQ]), (uint32_t)((t / C::kQ - 1) & 1));
         if (!ok) return;
         load(qslot(t), &tq, it.r0 + 128 * w, it.bk, &S.q_full[t % C::kQ]);
         ++t;
@@ -125,7 +193,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int j = 0; j < nkv && ok; ++j) {
           if (j == 2 && it.act1) load_q(1);
           if (f >= C::kKv && ok)
-            ok = mbar_wait_bounded(smem_u32(&S.kv_empty[f % C::kKv]), (uint32_t)((f / C::kKv - 1) & 1));
+            ok = mbar_wait(smem_u32(&S.kv_empty[f % C::kKv]), (uint32_t)((f / C::kKv - 1) & 1));
           if (!ok) break;
           load(kvslot(f), (j & 1) ? &tv : &tk, (it.kt0 + j / 2) * 128, it.bk, &S.kv_full[f % C::kKv]);
           ++f;
@@ -134,9 +202,9 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       }
       // no copy may still be landing when the CTA exits
       for (int i = t > C::kQ ? t - C::kQ : 0; i < t; ++i)
-        if (!mbar_wait_bounded(smem_u32(&S.q_full[i % C::kQ]), (uint32_t)((i / C::kQ) & 1))) ok = false;
+        if (!mbar_wait(smem_u32(&S.q_full[i % C::kQ]), (uint32_t)((i / C::kQ) & 1))) ok = false;
       for (int i = f > C::kKv ? f - C::kKv : 0; i < f; ++i)
-        if (!mbar_wait_bounded(smem_u32(&S.kv_full[i % C::kKv]), (uint32_t)((i / C::kKv) & 1))) ok = false;
+        if (!mbar_wait(smem_u32(&S.kv_full[i % C::kKv]), (uint32_t)((i / C::kKv) & 1))) ok = false;
     }
   } else if (warp == kWarpMma) {
     // the whole warp walks; one lane issues
@@ -149,7 +217,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     int pf = 0, pnt = 0;     // the pending product's V tile and its 16-key steps
     bool pfirst = false, plast = false, pfree = false;
     auto wait = [&](uint64_t* bar, int phase) {
-      return ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)(phase & 1)));
+      return ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), (uint32_t)(phase & 1)));
     };
     auto pv = [&](int w) {   // O_w (+)= P_w V of the previous step
       if (!pend[w]) return;
@@ -212,7 +280,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     for (int w = 0; w < 2 && ok; ++w) pv(w);
     // every MMA of this CTA has completed before tensor memory is freed
     tc_commit_by(lead, smem_u32(&S.done));
-    if (!mbar_wait_bounded(smem_u32(&S.done), 0)) ok = false;
+    if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
   } else if (warp == kWarpClean) {
     if (clean) {
       int f = 0;
@@ -228,7 +296,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const bool on = key < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + key] != 0);
             word[c] = __ballot_sync(0xffffffffu, on);
           }
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.kv_full[slot]), (uint32_t)(((f + 1) / C::kKv) & 1)));
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.kv_full[slot]), (uint32_t)(((f + 1) / C::kKv) & 1)));
           if (!ok) break;
           const int rows = 16 * it.steps(j);
           unsigned char* v = sm + (kvslot(f + 1) - base);
@@ -254,7 +322,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       for (; ok && it.next();) {
         if (it.nkt == 0) continue;
         for (int w = 0; w < (it.act1 ? 2 : 1) && ok; ++w, ++t) {
-          ok = mbar_wait_bounded(smem_u32(&S.o_staged[w]), (uint32_t)(n[w] & 1));
+          ok = mbar_wait(smem_u32(&S.o_staged[w]), (uint32_t)(n[w] & 1));
           if (!ok) break;
           ++n[w];
           if (p.nks == 1) {
@@ -307,9 +375,9 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       for (int j = 0; j < it.nkt && ok; ++j, ++ns) {
         const int nch = (it.steps(j) + 1) / 2;  // chunks of 32 keys
         const int slot = (frun + 2 * j + 1) % C::kKv;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.s_full[w]), (uint32_t)(ns & 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.s_full[w]), (uint32_t)(ns & 1)));
         if (ok && clean)
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.kv_clean[slot]),
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.kv_clean[slot]),
                                                          (uint32_t)(((frun + 2 * j + 1) / C::kKv) & 1)));
         if (!ok) break;
         tc_fence_after();
@@ -320,6 +388,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         };
         // the row's maximum
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
         for (int c = 0; c < nch; ++c) {
           const uint32_t bits = seen(c);
           float x[32];
@@ -353,6 +422,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         // P = 2^(s sc2 - m), over the S columns already read
         const uint64_t nm2 = f2_make(-mb, -mb);
         uint64_t sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll 1
         for (int c = 0; c < nch; ++c) {
           const uint32_t bits = seen(c);
           float x[32];
@@ -381,7 +451,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       }
       if (!ok) break;
       // ------------------------------------------------------------ epilogue
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&S.o_full[w]), (uint32_t)(no & 1)));
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.o_full[w]), (uint32_t)(no & 1)));
       if (!ok) break;
       ++no;
       tc_fence_after();
@@ -439,14 +509,15 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 }
 
 template <int D>
-cudaError_t launch_typed(const CrossParams& p, const CUtensorMap* maps, cudaStream_t s) {
-  const size_t smem = 1024 + Cfg<D>::kEnd + sizeof(Shared);
+cudaError_t launch_typed(CrossParams p, const CUtensorMap* maps, cudaStream_t s) {
+  constexpr size_t smem = 1024 + Cfg<D>::kEnd + sizeof(Shared);
   cudaError_t e = cudaFuncSetAttribute(cross_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)p.B * p.H * p.nks * ((p.N + 255) / 256);
+  const int64_t items = (int64_t)p.B * p.H * p.nks * cross_tiles(p.N, 256);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int grid = (int)(items < kCrossSms ? items : kCrossSms);
-  cross_fwd_tc_kernel<D><<<grid, kThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], p, (int)items);
+  p.runs = cross_runs(items, grid);
+  cross_fwd_tc_kernel<D><<<grid, kThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], p);
   return cudaGetLastError();
 }
 
@@ -454,8 +525,8 @@ cudaError_t launch_typed(const CrossParams& p, const CUtensorMap* maps, cudaStre
 
 CrossPlan cross_tc_fwd_plan(long long BH, int N, int S) {
   // cut the keys where the row tiles leave SMs without an item
-  const long long units = BH * (((long long)N + 255) / 256), kt = ((long long)S + 127) / 128;
-  long long nks = kCrossSms / units;
+  const int64_t units = BH * cross_tiles(N, 256), kt = cross_tiles(S, 128);
+  int64_t nks = kCrossSms / units;
   if (nks > kt) nks = kt;
   return {nks < 1 ? 1 : (int)nks, 1};
 }

@@ -23,54 +23,17 @@ __device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0
 // (addresses stay below 2^18, so the field takes the sum).
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc0, uint32_t a) { return desc0 + (a >> 4); }
 
-// The items of a CTA, in order: 256 query rows of one key head against one
-// range of its key tiles.  Every warp role walks them by itself; rows are
-// innermost, so items of the same keys follow one another (a run).
-struct CrossItems {
-  const CrossParams& p;
-  int i, end, nqp, cap;
-  int R;                       // query rows of a key head
-  size_t rows;                 // and of all of them
-  int bk, b, split, r0, len;   // the item: key head, batch entry, key range, first row, keys seen at the front
-  int kt0, nkt;                // its key tiles
-  bool act1;                   // whether its second tile of 128 rows has any
-  bool new_run, last_of_run;
-  bool resident;               // its key tiles fit in the ring: loaded once for the run
-
-  __device__ __forceinline__ CrossItems(const CrossParams& p_, int items, int cap_) : p(p_), cap(cap_) {
-    R = p.N;
-    rows = (size_t)p.B * p.H * R;
-    nqp = (R + 255) / 256;
-    i = (int)((long long)items * blockIdx.x / gridDim.x) - 1;
-    end = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
-    bk = -1;
-    split = -1;
+// mbar_wait_bounded in few instructions: these kernels wait in many places,
+// and their warp roles share the instruction cache.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {  // a poll suspends the warp
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) return false;
   }
-  __device__ __forceinline__ bool next() {
-    if (++i >= end) return false;
-    const int run = i / nqp, qp = i - run * nqp;
-    const int nbk = run / p.nks, nsplit = run - nbk * p.nks;
-    new_run = nbk != bk || nsplit != split;
-    last_of_run = qp == nqp - 1 || i + 1 == end;
-    if (new_run) {
-      bk = nbk;
-      split = nsplit;
-      b = bk / p.H;
-      len = cross_len(p, b);
-      const int kt = (len + 127) / 128;
-      kt0 = (int)((long long)kt * split / p.nks);
-      nkt = (int)((long long)kt * (split + 1) / p.nks) - kt0;
-      resident = nkt <= cap;
-    }
-    r0 = qp * 256;
-    act1 = r0 + 128 < R;
-    return true;
-  }
-  // 16-key steps of key tile j of the item
-  __device__ __forceinline__ int steps(int j) const {
-    const int n = len - (kt0 + j) * 128;
-    return n >= 128 ? 8 : (n + 15) >> 4;
-  }
-};
+  return true;
+}
 
 }  // namespace llsa
