@@ -559,71 +559,55 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             c2 = f2_make(c0, c0);
             have_c = true;
           }
-          const int left = it.len - (it.n0 + j) * 64;
+          const int nt = it.steps(j), left = it.len - (it.n0 + j) * 64;
+          if (clean || left < 64) {
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            const int m = left - 32 * c;
-            if (m <= 0) break;
-            uint32_t bits = m >= 32 ? 0xffffffffu : (1u << m) - 1u;
-            if (clean) bits = S.bits[s % NS][c];
-            if (!have_c) {
-              float d[32];
-              tmem_ld32(ts + 64, d);
-              tmem_wait_ld();
-              if (bits != 0xffffffffu) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (((bits >> i) & 1u) == 0u) d[i] = 0.f;
-              }
-              uint64_t t = f2_make(d[0], d[1]);
-#pragma unroll
-              for (int i = 2; i < 32; i += 2) t = f2_add(t, f2_make(d[i], d[i + 1]));
-              const float2 u = f2_split(t);
-              const float c0 = (u.x + u.y) * (1.f / (float)max(1, __popc(bits)));
-              c2 = f2_make(c0, c0);
-              have_c = true;
-              if (a >= C::kSums && !wait(&S.x_read[par], a / C::kSums - 1)) break;
-              S.q.c[par][r] = c0;
-              mbar_arrive(smem_u32(&S.c_full[par]));
+            for (int c = 0; c < nt; ++c) {
+              const uint32_t bits = clean ? (S.bits[s % NS][c >> 1] >> (16 * (c & 1))) & 0xffffu
+                                          : (left - 16 * c >= 16 ? 0xffffu : (1u << (left - 16 * c)) - 1u);
+              if (bits == 0xffffu) continue;
+              hide16(ts + 16 * c, bits, -INFINITY);
+              hide16(ts + 64 + 16 * c, bits, 0.f);
             }
-            float x[32];
-            uint32_t pk[16];
-            tmem_ld32(ts + 32 * c, x);
+          }
+          if (!have_c) {
+            float d[16];
+            tmem_ld16(ts + 64, d);
             tmem_wait_ld();
-            if (bits != 0xffffffffu) {
+            float t = 0.f;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (((bits >> i) & 1u) == 0u) x[i] = -INFINITY;
-            }
+            for (int i = 0; i < 16; ++i) t += d[i];
+            uint32_t bits = 0xffffu;
+            if (clean) bits = S.bits[s % NS][0] & 0xffffu;
+            else if (left < 16) bits = (1u << left) - 1u;
+            const float c0 = t / (float)max(1, __popc(bits));
+            c2 = f2_make(c0, c0);
+            have_c = true;
+            if (a >= C::kSums && !wait(&S.x_read[par], a / C::kSums - 1)) break;
+            S.q.c[par][r] = c0;
+            mbar_arrive(smem_u32(&S.c_full[par]));
+          }
+#pragma unroll 1
+          for (int c = 0; c < nt; ++c) {  // 16 keys
+            float x[16], d[16];
+            tmem_ld16(ts + 16 * c, x);
+            tmem_ld16(ts + 64 + 16 * c, d);
+            tmem_wait_ld();
+            uint32_t pk[8], dk[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const float2 e = f2_split(f2_fma(f2_make(x[2 * i], x[2 * i + 1]), sc2x2, nl2));
-              x[2 * i] = ex2_approx(e.x);
-              x[2 * i + 1] = ex2_approx(e.y);
-              ls = f2_add(ls, f2_make(x[2 * i], x[2 * i + 1]));
-              pk[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+              const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+              const uint64_t pp = f2_make(p0, p1);
+              const uint64_t t = f2_mul(pp, f2_sub(f2_make(d[2 * i], d[2 * i + 1]), c2));
+              ls = f2_add(ls, pp);
+              ds = f2_add(ds, t);
+              const float2 tt = f2_split(t);
+              pk[i] = pack_bf16(p0, p1);
+              dk[i] = pack_bf16(tt.x, tt.y);
             }
-            tmem_st16u(ts + 16 * c, pk);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float d[16];
-              tmem_ld16(ts + 64 + 32 * c + 16 * h, d);
-              tmem_wait_ld();
-              if (bits != 0xffffffffu) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (((bits >> (16 * h + i)) & 1u) == 0u) d[i] = 0.f;
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint64_t t = f2_mul(f2_make(x[16 * h + 2 * i], x[16 * h + 2 * i + 1]),
-                                          f2_sub(f2_make(d[2 * i], d[2 * i + 1]), c2));
-                ds = f2_add(ds, t);
-                const float2 tt = f2_split(t);
-                pk[8 * h + i] = pack_bf16(tt.x, tt.y);
-              }
-            }
-            tmem_st16u(ts + 64 + 16 * c, pk);
+            tmem_st8u(ts + 8 * c, pk);
+            tmem_st8u(ts + 64 + 8 * c, dk);
           }
           if (!ok) break;
           tmem_wait_st();
@@ -644,39 +628,31 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           tc_fence_after();
           const float2* side = S.side[s % NS];
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float x[32], d[32];
-            tmem_ld32(ts + 32 * c, x);
-            tmem_ld32(ts + 64 + 32 * c, d);
+          for (int c = 0; c < 4; ++c) {  // 16 queries
+            float x[16], d[16];
+            tmem_ld16(ts + 16 * c, x);
+            tmem_ld16(ts + 64 + 16 * c, d);
             tmem_wait_ld();
-            uint32_t pk[16];
+            uint32_t pk[8], dk[8];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float4 nl = *reinterpret_cast<const float4*>(side + 16 * c + i);
+            for (int i = 0; i < 8; i += 2) {
+              const float4 nl = *reinterpret_cast<const float4*>(side + 8 * c + i);
+              const float4 de = *reinterpret_cast<const float4*>(side + 32 + 8 * c + i);
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const int e = 2 * (i + u);
                 const float2 t = f2_split(f2_fma(f2_make(x[e], x[e + 1]), sc2x2,
                                                  u ? f2_make(nl.z, nl.w) : f2_make(nl.x, nl.y)));
-                x[e] = ex2_approx(t.x);
-                x[e + 1] = ex2_approx(t.y);
-                pk[i + u] = pack_bf16(x[e], x[e + 1]);
-              }
-            }
-            tmem_st16u(ts + 16 * c, pk);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float4 de = *reinterpret_cast<const float4*>(side + 32 + 16 * c + i);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int e = 2 * (i + u);
-                const float2 q = f2_split(f2_mul(f2_make(x[e], x[e + 1]),
+                const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
+                const float2 q = f2_split(f2_mul(f2_make(p0, p1),
                                                  f2_sub(f2_make(d[e], d[e + 1]),
                                                         u ? f2_make(de.z, de.w) : f2_make(de.x, de.y))));
-                pk[i + u] = pack_bf16(q.x, q.y);
+                pk[i + u] = pack_bf16(p0, p1);
+                dk[i + u] = pack_bf16(q.x, q.y);
               }
             }
-            tmem_st16u(ts + 64 + 16 * c, pk);
+            tmem_st8u(ts + 8 * c, pk);
+            tmem_st8u(ts + 64 + 8 * c, dk);
           }
           tmem_wait_st();
           tc_fence_before();

@@ -381,24 +381,22 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                                                          (uint32_t)(((frun + 2 * j + 1) / C::kKv) & 1)));
         if (!ok) break;
         tc_fence_after();
-        auto seen = [&](int c) {  // the keys of chunk c that are seen
-          if (clean) return S.bits[slot][c];
-          const int n = it.len - (it.kt0 + j) * 128 - 32 * c;
-          return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
-        };
+        const int left = it.len - (it.kt0 + j) * 128;
+        if (clean || left < 128) {
+#pragma unroll 1
+          for (int c = 0; c < 2 * nch; ++c) {
+            const uint32_t bits = clean ? (S.bits[slot][c >> 1] >> (16 * (c & 1))) & 0xffffu
+                                        : (left - 16 * c >= 16 ? 0xffffu : (left <= 16 * c ? 0u : (1u << (left - 16 * c)) - 1u));
+            if (bits != 0xffffu) hide16(ts + 16 * c, bits, -INFINITY);
+          }
+        }
         // the row's maximum
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
-          const uint32_t bits = seen(c);
           float x[32];
           tmem_ld32(ts + 32 * c, x);
           tmem_wait_ld();
-          if (bits != 0xffffffffu) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (((bits >> i) & 1u) == 0u) x[i] = -INFINITY;
-          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
         }
@@ -424,15 +422,9 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         uint64_t sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
-          const uint32_t bits = seen(c);
           float x[32];
           tmem_ld32(ts + 32 * c, x);
           tmem_wait_ld();
-          if (bits != 0xffffffffu) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (((bits >> i) & 1u) == 0u) x[i] = -INFINITY;
-          }
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {

@@ -36,4 +36,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// Puts `with` over the 16 scores (or dP) of a row at ts whose bit of `seen` is
+// off.  Rare: tiles with keys that are not seen.
+static __device__ __noinline__ void hide16(uint32_t ts, uint32_t seen, float with) {
+  float x[16];
+  tmem_ld16(ts, x);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = (seen >> i) & 1u ? x[i] : with;
+  tmem_st16(ts, x);
+  tmem_wait_st();
+}
+
 }  // namespace llsa

@@ -183,6 +183,13 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+// registers -> TMEM: 8 packed 32-bit words of this lane
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // registers -> TMEM: N (16 or 32) packed 32-bit words of this lane
 template <int N>
 __device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t* v) {
