@@ -28,7 +28,8 @@
 //   the groups' first;
 //   four for the epilogue, so that the groups go on with the next item;
 //   load    TMA loads of A (two buffers) and N (a ring);
-//   mma     issues the MMAs;
+//   mma     issues S and dP; prod the products.  One warp for both would leave
+//           the tensor cores idle between its waits;
 //   aux     first pass: with lengths or a mask, the bits of the keys seen and
 //           zeros over the K rows that are not (their dS is zero, and zero
 //           times NaN is NaN); second pass: lse and Delta of the queries that
@@ -52,7 +53,7 @@ struct Cfg {
   // tensor memory has 512 columns: accA and accB take 2 D, a stage 128
   static constexpr int kStages = (D == 64) ? 3 : 2;
   static constexpr int kEpi = kStages * 4;  // first epilogue warp
-  static constexpr int kLoad = kEpi + 4, kMma = kLoad + 1, kAux = kMma + 1;
+  static constexpr int kLoad = kEpi + 4, kMma = kLoad + 1, kProd = kMma + 1, kAux = kProd + 1;
   static constexpr int kThreads = (kAux + 1) * 32;
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
@@ -228,121 +229,148 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       mbar_init(smem_u32(&S.x_full[i]), NG * 128);
       mbar_init(smem_u32(&S.x_read[i]), 128);
     }
-    mbar_init(smem_u32(&S.done), 1);
+    mbar_init(smem_u32(&S.done), 2);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = uniform(S.tmem_base);
-  auto abuf = [&](int a) { return base + (uint32_t)(a & 1) * 2 * C::kA; };
-  auto nslot = [&](int s) { return base + C::kOffN + (uint32_t)(s % NS) * 2 * C::kN; };
-  auto wait = [&](uint64_t* bar, int phase) {  // by whole warps
-    return ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), (uint32_t)(phase & 1)));
+  auto abuf = [&](uint32_t i) { return base + i * 2 * C::kA; };
+  auto nslot = [&](uint32_t i) { return base + C::kOffN + i * 2 * C::kN; };
+  const uint32_t a_full = smem_u32(S.a_full), a_empty = smem_u32(S.a_empty), n_full = smem_u32(S.n_full),
+                 n_empty = smem_u32(S.n_empty), n_aux = smem_u32(S.n_aux), s_full = smem_u32(S.s_full),
+                 p_full = smem_u32(S.p_full), acc_full = smem_u32(&S.acc_full), acc_free = smem_u32(&S.acc_free),
+                 c_full = smem_u32(S.c_full), x_full = smem_u32(S.x_full), x_read = smem_u32(S.x_read);
+  // Waits of whole warps.  A look at a barrier takes 150 cycles even where its
+  // phase is over: where it can, a warp looks before it does something else
+  // (or at two barriers at once) and takes the answer afterwards.
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+  auto look = [&](uint32_t bar, uint32_t parity) { return mbar_look(bar, parity); };
+  auto finish = [&](bool seen, uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, seen) || wait(bar, parity);
   };
   BwdItems<kDq> it(p);
 
   if (warp == C::kLoad) {
     if (lane == 0) {
-      int a = 0, s = 0;  // items and streamed tiles so far
+      Ring<2> ra;
+      Ring<NS> rn;
+      // a buffer's first round waits for the phase before the first, which is over
       for (; ok && it.next();) {
         if (it.n == 0) continue;
-        uint64_t* full = &S.a_full[a & 1];
-        if (a >= 2) ok = mbar_wait(smem_u32(&S.a_empty[a & 1]), (uint32_t)((a / 2 - 1) & 1));
+        ok = mbar_wait(ra.at(a_empty), ra.parity ^ 1u);
         if (!ok) break;
-        mbar_arrive_expect_tx(smem_u32(full), 2 * C::kA);
+        mbar_arrive_expect_tx(ra.at(a_full), 2 * C::kA);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          tma_load_3d(abuf(a) + h * 16384, &ta1, 64 * h, it.r0, it.bk, smem_u32(full));
-          tma_load_3d(abuf(a) + C::kA + h * 16384, &ta2, 64 * h, it.r0, it.bk, smem_u32(full));
+          tma_load_3d(abuf(ra.i) + h * 16384, &ta1, 64 * h, it.r0, it.bk, ra.at(a_full));
+          tma_load_3d(abuf(ra.i) + C::kA + h * 16384, &ta2, 64 * h, it.r0, it.bk, ra.at(a_full));
         }
-        ++a;
-        for (int j = 0; j < it.n; ++j, ++s) {
-          if (s >= NS) ok = mbar_wait(smem_u32(&S.n_empty[s % NS]), (uint32_t)((s / NS - 1) & 1));
+        ra.next();
+        for (int j = 0; j < it.n; ++j) {
+          ok = mbar_wait(rn.at(n_empty), rn.parity ^ 1u);
           if (!ok) break;
-          full = &S.n_full[s % NS];
-          mbar_arrive_expect_tx(smem_u32(full), 2 * C::kN);
+          mbar_arrive_expect_tx(rn.at(n_full), 2 * C::kN);
 #pragma unroll
           for (int h = 0; h < H; ++h) {
-            tma_load_3d(nslot(s) + h * 8192, &tn1, 64 * h, (it.n0 + j) * 64, it.bk, smem_u32(full));
-            tma_load_3d(nslot(s) + C::kN + h * 8192, &tn2, 64 * h, (it.n0 + j) * 64, it.bk, smem_u32(full));
+            tma_load_3d(nslot(rn.i) + h * 8192, &tn1, 64 * h, (it.n0 + j) * 64, it.bk, rn.at(n_full));
+            tma_load_3d(nslot(rn.i) + C::kN + h * 8192, &tn2, 64 * h, (it.n0 + j) * 64, it.bk, rn.at(n_full));
           }
+          rn.next();
         }
       }
-      // no copy may still be landing when the CTA exits
-      for (int i = a > 2 ? a - 2 : 0; i < a; ++i)
-        if (!mbar_wait(smem_u32(&S.a_full[i & 1]), (uint32_t)((i / 2) & 1))) ok = false;
-      for (int i = s > NS ? s - NS : 0; i < s; ++i)
-        if (!mbar_wait(smem_u32(&S.n_full[i % NS]), (uint32_t)((i / NS) & 1))) ok = false;
+      // no copy may still be landing when the CTA exits: of every place, the
+      // last round that was begun
+      for (int i = 0; i < 2; ++i, ra.next())
+        if (!mbar_wait(ra.at(a_full), ra.parity ^ 1u)) ok = false;
+      for (int i = 0; i < NS; ++i, rn.next())
+        if (!mbar_wait(rn.at(n_full), rn.parity ^ 1u)) ok = false;
     }
   } else if (warp == C::kMma) {
-    // the whole warp walks; one lane issues
-    constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1, 0);
-    constexpr uint32_t kSecond = kDq ? 0 : C::kN;  // accB's right side: N1 or N2
-    const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, 8192, 1024);
+    // S and dP; the whole warp walks, one lane issues
+    const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);
     const uint32_t lead = elect_lane();
-    int a = 0, s = 0;        // items; tiles whose S and dP are issued
-    int ps = 0, pa = 0;      // tiles, and items, whose products are
-    uint32_t queue = 0;      // of the tiles in between, the oldest on top of the lowest byte: 16-row steps | first | last
-    auto products = [&]() {  // accA (+)= dS N1, accB (+)= P N1 or N2 of tile ps
-      const uint32_t info = (queue >> (8 * (s - ps - 1))) & 255u;
-      const int g = ps % NG, pnt = (int)(info & 7u);
-      const bool first = (info & 8u) != 0;
-      if (kDq && clean && !wait(&S.n_aux[ps % NS], ps / NS)) return;
-      if (!wait(&S.p_full[g], ps / NG)) return;
-      if (first) {
-        if (pa > 0 && !wait(&S.acc_free, pa - 1)) return;
-        ++pa;
-      }
-      tc_fence_after();
-      const uint32_t ts = tbase + (uint32_t)g * 128;
-      const uint64_t n1 = desc_at(nmaj, nslot(ps)), n2 = desc_at(n1, kSecond);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k >= pnt) break;
-        const uint32_t add = !first || k > 0;
-        tc_mma_f16_ts_by(lead, tbase + C::kColAcc + D, ts + k * 8, desc_at(n2, k * 2048), idesc_acc, add);
-        tc_mma_f16_ts_by(lead, tbase + C::kColAcc, ts + 64 + k * 8, desc_at(n1, k * 2048), idesc_acc, add);
-      }
-      tc_commit_by(lead, smem_u32(&S.n_empty[ps % NS]));
-      if ((info & 16u) != 0) tc_commit_by(lead, smem_u32(&S.acc_full));
-      ++ps;
-    };
+    Ring<2> ra;
+    Ring<NS> rn, pn;  // tiles; and the tiles NG before, whose stages these take
+    Ring<NG> rs;
+    int fresh = NG;   // stages not used yet
     for (; ok && it.next();) {
       const int n = uniform(it.n);
       if (n == 0) continue;
-      for (int j = 0; j < n && ok; ++j) {
-        if (s - ps == NG) products();  // its stage is the next tile's
-        if (!ok) break;
-        if (j == 0 && !wait(&S.a_full[a & 1], a / 2)) break;
-        if (!wait(&S.n_full[s % NS], s / NS)) break;
+      if (!wait(ra.at(a_full), ra.parity)) break;
+      const uint64_t a1 = desc_at(kmaj, abuf(ra.i));
+      for (int j = 0; j < n; ++j) {
+        const bool n_seen = look(rn.at(n_full), rn.parity);
+        if (fresh > 0) {
+          --fresh;
+        } else {  // the products that read the stage are done
+          if (!wait(pn.at(n_empty), pn.parity)) break;
+          pn.next();
+        }
+        if (!finish(n_seen, rn.at(n_full), rn.parity)) break;
         tc_fence_after();
-        const uint32_t ts = tbase + (uint32_t)(s % NG) * 128;
-        const int nt = uniform(it.steps(j));
-        const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
-        const uint64_t a1 = desc_at(kmaj, abuf(a)), n1 = desc_at(kmaj, nslot(s));
+        const uint32_t ts = tbase + rs.i * 128;
+        const uint32_t idesc_s = idesc_bf16_f32(128, 16 * (kDq ? uniform(it.steps(j)) : 4), 0, 0);
+        const uint64_t n1 = desc_at(kmaj, nslot(rn.i));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int w = 0; w < 2; ++w)
             tc_mma_f16_by(lead, ts + 64 * w, desc_at(a1, w * C::kA + (ks >> 2) * 16384 + (ks & 3) * 32),
                           desc_at(n1, w * C::kN + (ks >> 2) * 8192 + (ks & 3) * 32), idesc_s, ks > 0);
-        tc_commit_by(lead, smem_u32(&S.s_full[s % NG]));
-        if (!kDq && j == n - 1) tc_commit_by(lead, smem_u32(&S.a_empty[a & 1]));
-        queue = (queue << 8) | (uint32_t)nt | (j == 0 ? 8u : 0u) | (j == n - 1 ? 16u : 0u);
-        ++s;
+        tc_commit_by(lead, rs.at(s_full));
+        rn.next();
+        rs.next();
       }
-      ++a;
+      if (!ok) break;
+      if (!kDq) tc_commit_by(lead, ra.at(a_empty));
+      ra.next();
     }
-    while (ok && ps < s) products();
     // every MMA of this CTA has completed before tensor memory is freed
     tc_commit_by(lead, smem_u32(&S.done));
     if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
+  } else if (warp == C::kProd) {
+    // accA (+)= dS N1, accB (+)= P N1 or N2
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1, 0);
+    constexpr uint32_t kSecond = kDq ? 0 : C::kN;
+    const uint64_t nmaj = smem_desc_sw128(0, 8192, 1024);
+    const uint32_t lead = elect_lane();
+    Ring<NS> rn;
+    Ring<NG> rs;
+    uint32_t acc_par = 1;  // of acc_free: the phase before the first is over
+    for (; ok && it.next();) {
+      const int n = uniform(it.n);
+      if (n == 0) continue;
+      for (int j = 0; j < n; ++j) {
+        if (kDq && clean && !wait(rn.at(n_aux), rn.parity)) break;
+        if (j == 0 && !wait(acc_free, acc_par)) break;
+        if (!wait(rs.at(p_full), rs.parity)) break;
+        tc_fence_after();
+        const uint32_t ts = tbase + rs.i * 128;
+        const int nt = kDq ? uniform(it.steps(j)) : 4;
+        const uint64_t n1 = desc_at(nmaj, nslot(rn.i)), n2 = desc_at(n1, kSecond);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= nt) break;
+          const uint32_t add = j > 0 || k > 0;
+          tc_mma_f16_ts_by(lead, tbase + C::kColAcc + D, ts + k * 8, desc_at(n2, k * 2048), idesc_acc, add);
+          tc_mma_f16_ts_by(lead, tbase + C::kColAcc, ts + 64 + k * 8, desc_at(n1, k * 2048), idesc_acc, add);
+        }
+        tc_commit_by(lead, rn.at(n_empty));
+        rn.next();
+        rs.next();
+      }
+      if (!ok) break;
+      acc_par ^= 1u;
+      tc_commit_by(lead, acc_full);
+    }
+    tc_commit_by(lead, smem_u32(&S.done));
+    if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
   } else if (warp == C::kAux) {
-    int s = 0;
+    Ring<NS> rn;
     for (; ok && (clean || !kDq) && it.next();) {
-      for (int j = 0; j < it.n && ok; ++j, ++s) {
-        const int slot = s % NS;
+      for (int j = 0; j < it.n && ok; ++j, rn.next()) {
         if (kDq) {
           uint32_t word[2];
 #pragma unroll
@@ -351,12 +379,12 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             const bool on = key < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + key] != 0);
             word[c] = __ballot_sync(0xffffffffu, on);
           }
-          if (!wait(&S.n_full[slot], s / NS)) break;
+          if (!wait(rn.at(n_full), rn.parity)) break;
           const int rows = 16 * it.steps(j);
-          unsigned char* k = sm + (nslot(s) - base);
+          unsigned char* k = sm + (nslot(rn.i) - base);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (lane == 0) S.bits[slot][c] = word[c];
+            if (lane == 0) S.bits[rn.i][c] = word[c];
             for (uint32_t off = ~word[c]; off != 0u; off &= off - 1) {  // one row at a time, 16 bytes a lane
               const int r = 32 * c + __ffs(off) - 1;
               if (r >= rows) break;
@@ -378,20 +406,23 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             nl.y = neg_lse2(p.lse_in[g + 1]);
             de.y = p.delta[g + 1];
           }
-          if (s >= NS && !wait(&S.n_empty[slot], s / NS - 1)) break;
-          S.side[slot][lane] = nl;
-          S.side[slot][32 + lane] = de;
+          if (!wait(rn.at(n_empty), rn.parity ^ 1u)) break;
+          S.side[rn.i][lane] = nl;
+          S.side[rn.i][32 + lane] = de;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&S.n_aux[slot]));
+        if (lane == 0) mbar_arrive(rn.at(n_aux));
       }
     }
   } else if (warp >= C::kEpi) {
     // ------------------------------------------------------------- epilogue
     const int q4 = warp & 3, r = q4 * 32 + lane;  // row of A = TMEM lane
     const uint32_t tacc = tbase + ((uint32_t)(q4 * 32) << 16) + C::kColAcc;
-    int a = 0, last_b = -1;
+    int last_b = -1;
     bool one = false;
+    Ring<2> ra;
+    Ring<C::kSums> rx;
+    uint32_t par = 0;  // of acc_full and staged: the item's
     for (; ok && it.next(); ) {
       const int row = it.r0 + r;
       const bool new_b = it.b != last_b;
@@ -416,25 +447,25 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           }
           continue;
         }
-        const int par = a % C::kSums;
-        if (!wait(&S.x_full[par], a / C::kSums)) break;
-        const float c0 = S.q.c[par][r];
+        if (!wait(rx.at(x_full), rx.parity)) break;
+        const float c0 = S.q.c[rx.i][r];
         float sp = 0.f, sd = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float2 x = S.q.sums[par][g][r];
+          const float2 x = S.q.sums[rx.i][g][r];
           sp += x.x;
           sd += x.y;
         }
-        mbar_arrive(smem_u32(&S.x_read[par]));
+        mbar_arrive(rx.at(x_read));
+        rx.next();
         const float delta = fmaf(c0, sp, sd), f = c0 - delta;
         if (valid) {
           if (p.nks > 1) p.part_s[it.split * rows + grow] = make_float4(c0, sp, sd, 1.f);
           else p.delta[grow] = delta;
         }
-        if (!wait(&S.acc_full, a)) break;
+        if (!wait(acc_full, par)) break;
         tc_fence_after();
-        unsigned char* stage = sm + (abuf(a) - base);  // A1, which no MMA reads any more
+        unsigned char* stage = sm + (abuf(ra.i) - base);  // A1, which no MMA reads any more
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float x[16], y[16];
@@ -463,22 +494,23 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           }
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&S.acc_free));
+        mbar_arrive(acc_free);
         fence_proxy_async_smem();  // generic writes -> TMA store
         mbar_arrive(smem_u32(&S.staged));
         if (q4 == 0) {
-          if (!wait(&S.staged, a)) break;
+          if (!wait(smem_u32(&S.staged), par)) break;
           if (lane == 0) {
             if (p.nks == 1) {
 #pragma unroll
-              for (int h = 0; h < H; ++h) tma_store_3d(&tdq, 64 * h, it.r0, it.bk, abuf(a) + h * 16384);
+              for (int h = 0; h < H; ++h) tma_store_3d(&tdq, 64 * h, it.r0, it.bk, abuf(ra.i) + h * 16384);
               bulk_commit_group();
               bulk_wait_read_all();
             }
-            mbar_arrive(smem_u32(&S.a_empty[a & 1]));
+            mbar_arrive(ra.at(a_empty));
           }
         }
-        ++a;
+        ra.next();
+        par ^= 1u;
       } else {
         // keys that are not seen: whatever their rows hold, it stays in them
         const bool seen = row < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + row] != 0);
@@ -497,8 +529,8 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           const int slot = (int)blockIdx.x - p.runs.cta_of((int64_t)it.i * it.nq);
           part_row = ((size_t)it.i * p.nz + slot) * 128 + r;
         }
-        if (!wait(&S.acc_full, a)) break;
-        ++a;
+        if (!wait(acc_full, par)) break;
+        par ^= 1u;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 2 * D; c += 32) {  // accA is dK, accB dV
@@ -524,7 +556,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           }
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&S.acc_free));
+        mbar_arrive(acc_free);
       }
     }
     if (kDq && r == 0) bulk_wait_all();
@@ -535,7 +567,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     const uint32_t ts = tbase + ((uint32_t)(q4 * 32) << 16) + (uint32_t)g * 128;
     const float sc2 = p.scale * kLog2e;
     const uint64_t sc2x2 = f2_make(sc2, sc2);
-    int a = 0, s = 0;
+    Ring<NS> rn;          // of this group's tiles
+    rn.next(g);
+    uint32_t turn = 0;    // parity of its stage
+    int j = g;            // its next tile of the item
+    Ring<C::kSums> rx;
     float lse_next = 0.f;
     if (kDq) lse_next = p.lse_in[it.peek(r)];
     for (; ok && it.next();) {
@@ -543,27 +579,26 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         const float lse = lse_next;
         lse_next = p.lse_in[it.peek(r)];
         if (it.n == 0) continue;
-        const int par = a % C::kSums;
         const float nl = it.r0 + r < p.N ? neg_lse2(lse) : -INFINITY;  // rows past the end: probability zero
         const uint64_t nl2 = f2_make(nl, nl);
         bool have_c = false;
         uint64_t c2 = 0, ls = 0, ds = 0;
-        for (int j = 0; j < it.n; ++j, ++s) {
-          if (s % NG != g) continue;
-          if (!wait(&S.s_full[g], s / NG)) break;
-          if (clean && !wait(&S.n_aux[s % NS], s / NS)) break;
-          tc_fence_after();
+        for (; j < it.n; j += NG, rn.next(NG), turn ^= 1u) {
+          const bool s_seen = look(s_full + 8 * g, turn);
+          if (clean && !wait(rn.at(n_aux), rn.parity)) break;
           if (!have_c && j > 0) {  // another group has the item's first tile
-            if (!wait(&S.c_full[par], a / C::kSums)) break;
-            const float c0 = S.q.c[par][r];
+            if (!wait(rx.at(c_full), rx.parity)) break;
+            const float c0 = S.q.c[rx.i][r];
             c2 = f2_make(c0, c0);
             have_c = true;
           }
+          if (!finish(s_seen, s_full + 8 * g, turn)) break;
+          tc_fence_after();
           const int nt = it.steps(j), left = it.len - (it.n0 + j) * 64;
           if (clean || left < 64) {
 #pragma unroll 1
             for (int c = 0; c < nt; ++c) {
-              const uint32_t bits = clean ? (S.bits[s % NS][c >> 1] >> (16 * (c & 1))) & 0xffffu
+              const uint32_t bits = clean ? (S.bits[rn.i][c >> 1] >> (16 * (c & 1))) & 0xffffu
                                           : (left - 16 * c >= 16 ? 0xffffu : (1u << (left - 16 * c)) - 1u);
               if (bits == 0xffffu) continue;
               hide16(ts + 16 * c, bits, -INFINITY);
@@ -578,14 +613,14 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
 #pragma unroll
             for (int i = 0; i < 16; ++i) t += d[i];
             uint32_t bits = 0xffffu;
-            if (clean) bits = S.bits[s % NS][0] & 0xffffu;
+            if (clean) bits = S.bits[rn.i][0] & 0xffffu;
             else if (left < 16) bits = (1u << left) - 1u;
             const float c0 = t / (float)max(1, __popc(bits));
             c2 = f2_make(c0, c0);
             have_c = true;
-            if (a >= C::kSums && !wait(&S.x_read[par], a / C::kSums - 1)) break;
-            S.q.c[par][r] = c0;
-            mbar_arrive(smem_u32(&S.c_full[par]));
+            if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
+            S.q.c[rx.i][r] = c0;
+            mbar_arrive(rx.at(c_full));
           }
 #pragma unroll 1
           for (int c = 0; c < nt; ++c) {  // 16 keys
@@ -612,21 +647,22 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           if (!ok) break;
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(smem_u32(&S.p_full[g]));
+          mbar_arrive(p_full + 8 * g);
         }
         if (!ok) break;
-        if (a >= C::kSums && !wait(&S.x_read[par], a / C::kSums - 1)) break;
+        j -= it.n;
+        if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
         const float2 l2 = f2_split(ls), d2 = f2_split(ds);
-        S.q.sums[par][g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
-        mbar_arrive(smem_u32(&S.x_full[par]));
-        ++a;
+        S.q.sums[rx.i][g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
+        mbar_arrive(rx.at(x_full));
+        rx.next();
       } else {
-        for (int j = 0; j < it.n; ++j, ++s) {
-          if (s % NG != g) continue;
-          if (!wait(&S.n_aux[s % NS], s / NS)) break;
-          if (!wait(&S.s_full[g], s / NG)) break;
+        for (; j < it.n; j += NG, rn.next(NG), turn ^= 1u) {
+          const bool x_seen = look(rn.at(n_aux), rn.parity), s_seen = look(s_full + 8 * g, turn);
+          if (!finish(x_seen, rn.at(n_aux), rn.parity)) break;
+          if (!finish(s_seen, s_full + 8 * g, turn)) break;
           tc_fence_after();
-          const float2* side = S.side[s % NS];
+          const float2* side = S.side[rn.i];
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {  // 16 queries
             float x[16], d[16];
@@ -656,8 +692,9 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           }
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(smem_u32(&S.p_full[g]));
+          mbar_arrive(p_full + 8 * g);
         }
+        j -= it.n;
       }
     }
   }

@@ -36,6 +36,36 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// Whether the phase is over, without waiting for it.
+__device__ __forceinline__ bool mbar_look(uint32_t bar, uint32_t parity) {
+  uint32_t over;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(over)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return over != 0;
+}
+
+// A place in a ring of N and the parity of the round it is in.
+template <int N>
+struct Ring {
+  uint32_t i = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t by = 1) {  // by <= N
+    i += by;
+    if (i >= N) {
+      i -= N;
+      parity ^= 1u;
+    }
+  }
+  // of the barriers at `bars`, this place's
+  __device__ __forceinline__ uint32_t at(uint32_t bars) const { return bars + 8u * i; }
+};
+
 // Puts `with` over the 16 scores (or dP) of a row at ts whose bit of `seen` is
 // off.  Rare: tiles with keys that are not seen.
 static __device__ __noinline__ void hide16(uint32_t ts, uint32_t seen, float with) {
