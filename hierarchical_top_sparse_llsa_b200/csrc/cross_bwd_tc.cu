@@ -41,6 +41,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "cross.cuh"
 #include "cross_tc.cuh"
 
@@ -49,7 +51,7 @@ namespace llsa {
 namespace {
 
 template <int D>
-struct Cfg {
+struct Sizes {
   // tensor memory has 512 columns: accA and accB take 2 D, a stage 128
   static constexpr int kStages = (D == 64) ? 3 : 2;
   static constexpr int kEpi = kStages * 4;  // first epilogue warp
@@ -58,26 +60,51 @@ struct Cfg {
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
   static constexpr int kSlots = (D == 64) ? 6 : 3;
-  static constexpr int kSums = (D == 64) ? 2 : 1;  // items whose row sums are held
-  static constexpr int kOffN = 4 * kA;     // two buffers of A1, A2
-  static constexpr int kEnd = kOffN + kSlots * 2 * kN;
   static constexpr uint32_t kColAcc = 128 * kStages;  // S | dP of each stage, accA | accB
 };
 
 template <typename C>
 struct Shared {
-  uint64_t a_full[2], a_empty[2], n_full[C::kSlots], n_empty[C::kSlots], n_aux[C::kSlots];
+  uint64_t a_full[C::kBufs], a_empty[C::kBufs], n_full[C::kSlots], n_empty[C::kSlots], n_aux[C::kSlots];
   uint64_t s_full[C::kStages], p_full[C::kStages], acc_full, acc_free, staged, done;
   uint64_t c_full[C::kSums], x_full[C::kSums], x_read[C::kSums];
   uint32_t tmem_base;
   uint32_t bits[C::kSlots][2];  // first pass: keys seen, by slot
-  union alignas(16) {
-    struct {
-      float c[C::kSums][128];                  // of the item's rows
-      float2 sums[C::kSums][C::kStages][128];  // each group's sum P, sum P (dP - c)
-    } q;
-    float2 side[C::kSlots][64];  // second pass, by slot: [0..31] -lse of 64 queries, [32..63] their Delta
-  };
+  typename C::Side side;
+};
+
+// Tiles whose lse and Delta the second pass's aux warp loads at once.
+constexpr int kAhead = 4;
+
+// First pass: of the rows of an item (two of them where there is room).
+template <int kSums, int kStages>
+struct RowSums {
+  static constexpr int kHeld = kSums;
+  float c[kSums][128];
+  float2 sums[kSums][kStages][128];  // each group's sum P, sum P (dP - c)
+};
+
+// Second pass: one more step of 16 along the heads' dimension adds -lse /
+// scale to S and -Delta to dP.  Its left side is all ones, its right side a
+// query's number in three bf16 terms and 13 zeros; both without a swizzle, 32
+// bytes a row.  (Read from shared memory by every thread, the two numbers of
+// each query would cost more cycles than the exponentials.)
+template <int kSlots>
+struct ColumnTerms {
+  static constexpr int kHeld = 1;
+  alignas(128) unsigned char ones[4096];
+  unsigned char terms[kSlots][2][2048];
+};
+
+template <int D, bool kDq>
+struct Cfg : Sizes<D> {
+  using Z = Sizes<D>;
+  // buffers of A1, A2: the second pass has few items
+  static constexpr int kBufs = (D == 64 || kDq) ? 2 : 1;
+  static constexpr int kOffN = kBufs * 2 * Z::kA;
+  static constexpr int kEnd = kOffN + Z::kSlots * 2 * Z::kN;
+  using Side = std::conditional_t<kDq, RowSums<(D == 64) ? 2 : 1, Z::kStages>, ColumnTerms<Z::kSlots>>;
+  static constexpr int kSums = Side::kHeld;
 };
 
 // The items of a CTA, in order.  First pass: 128 query rows against one range
@@ -170,6 +197,14 @@ struct BwdItems {
 // -lse in units of log2; without keys (lse = -inf) every probability is zero.
 __device__ __forceinline__ float neg_lse2(float lse) { return lse == -INFINITY ? lse : -lse * kLog2e; }
 
+// x as the sum of three bf16 (infinities and NaN as they are), and a zero.
+__device__ __forceinline__ uint2 three_terms(float x) {
+  const float h = bf16x2_lo(pack_bf16(x, 0.f));
+  const float m0 = fabsf(h) < INFINITY ? x - h : 0.f;
+  const float m = bf16x2_lo(pack_bf16(m0, 0.f));
+  return make_uint2(pack_bf16(h, m), pack_bf16(m0 - m, 0.f));
+}
+
 // Whether b sees at most one key (a whole warp asks).
 __device__ __forceinline__ bool sees_one(const CrossParams& p, int b, int len) {
   if (p.mask == nullptr || len <= 1) return len <= 1;
@@ -190,11 +225,11 @@ __device__ __forceinline__ bool sees_one(const CrossParams& p, int b, int len) {
 }
 
 template <int D, bool kDq>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, kDq>::kThreads, 1)
 cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap ta2,
                     const __grid_constant__ CUtensorMap tn1, const __grid_constant__ CUtensorMap tn2,
                     const __grid_constant__ CUtensorMap tdq, CrossParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kDq>;
   constexpr int H = D / 64;  // 64-column halves of a tile
   constexpr int NS = C::kSlots, NG = C::kStages;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -208,7 +243,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     tmem_alloc(smem_u32(&S.tmem_base), 512);
     tmem_relinquish();
   } else if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(smem_u32(&S.a_full[i]), 1);
       mbar_init(smem_u32(&S.a_empty[i]), 1);
     }
@@ -232,6 +267,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     mbar_init(smem_u32(&S.done), 2);
     fence_mbar_init();
   }
+  if constexpr (!kDq) {
+    uint32_t* x = reinterpret_cast<uint32_t*>(&S.side);
+    for (int i = tid; i < (int)sizeof(S.side) / 4; i += C::kThreads) x[i] = i < 1024 ? 0x3f803f80u : 0u;
+    fence_proxy_async_smem();  // generic writes -> MMA operand reads
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -254,7 +294,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
 
   if (warp == C::kLoad) {
     if (lane == 0) {
-      Ring<2> ra;
+      Ring<C::kBufs> ra;
       Ring<NS> rn;
       // a buffer's first round waits for the phase before the first, which is over
       for (; ok && it.next();) {
@@ -282,7 +322,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       }
       // no copy may still be landing when the CTA exits: of every place, the
       // last round that was begun
-      for (int i = 0; i < 2; ++i, ra.next())
+      for (int i = 0; i < C::kBufs; ++i, ra.next())
         if (!mbar_wait(ra.at(a_full), ra.parity ^ 1u)) ok = false;
       for (int i = 0; i < NS; ++i, rn.next())
         if (!mbar_wait(rn.at(n_full), rn.parity ^ 1u)) ok = false;
@@ -291,7 +331,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     // S and dP; the whole warp walks, one lane issues
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);
     const uint32_t lead = elect_lane();
-    Ring<2> ra;
+    Ring<C::kBufs> ra;
     Ring<NS> rn, pn;  // tiles; and the tiles NG before, whose stages these take
     Ring<NG> rs;
     int fresh = NG;   // stages not used yet
@@ -301,7 +341,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
       if (!wait(ra.at(a_full), ra.parity)) break;
       const uint64_t a1 = desc_at(kmaj, abuf(ra.i));
       for (int j = 0; j < n; ++j) {
-        const bool n_seen = look(rn.at(n_full), rn.parity);
+        const bool n_seen = look(rn.at(n_full), rn.parity), x_seen = kDq || look(rn.at(n_aux), rn.parity);
         if (fresh > 0) {
           --fresh;
         } else {  // the products that read the stage are done
@@ -309,6 +349,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           pn.next();
         }
         if (!finish(n_seen, rn.at(n_full), rn.parity)) break;
+        if (!kDq && !finish(x_seen, rn.at(n_aux), rn.parity)) break;
         tc_fence_after();
         const uint32_t ts = tbase + rs.i * 128;
         const uint32_t idesc_s = idesc_bf16_f32(128, 16 * (kDq ? uniform(it.steps(j)) : 4), 0, 0);
@@ -319,6 +360,12 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           for (int w = 0; w < 2; ++w)
             tc_mma_f16_by(lead, ts + 64 * w, desc_at(a1, w * C::kA + (ks >> 2) * 16384 + (ks & 3) * 32),
                           desc_at(n1, w * C::kN + (ks >> 2) * 8192 + (ks & 3) * 32), idesc_s, ks > 0);
+        if constexpr (!kDq) {
+          const uint64_t x = smem_desc_plain(smem_u32(S.side.ones), 128, 256);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            tc_mma_f16_by(lead, ts + 64 * w, x, desc_at(x, 4096 + rn.i * 4096 + w * 2048), idesc_s, 1);
+        }
         tc_commit_by(lead, rs.at(s_full));
         rn.next();
         rs.next();
@@ -369,9 +416,9 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
   } else if (warp == C::kAux) {
     Ring<NS> rn;
-    for (; ok && (clean || !kDq) && it.next();) {
-      for (int j = 0; j < it.n && ok; ++j, rn.next()) {
-        if (kDq) {
+    if constexpr (kDq) {
+      for (; ok && clean && it.next();) {
+        for (int j = 0; j < it.n && ok; ++j, rn.next()) {
           uint32_t word[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -393,25 +440,43 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             }
           }
           fence_proxy_async_smem();  // generic writes -> MMA operand reads
-        } else {
-          const int row = (it.n0 + j) * 64 + 2 * lane;
-          const size_t g = (size_t)it.bk * p.N + row;
-          // rows past the end: probability zero
-          float2 nl = make_float2(-INFINITY, -INFINITY), de = make_float2(0.f, 0.f);
-          if (row < p.N) {
-            nl.x = neg_lse2(p.lse_in[g]);
-            de.x = p.delta[g];
-          }
-          if (row + 1 < p.N) {
-            nl.y = neg_lse2(p.lse_in[g + 1]);
-            de.y = p.delta[g + 1];
-          }
-          if (!wait(rn.at(n_empty), rn.parity ^ 1u)) break;
-          S.side[rn.i][lane] = nl;
-          S.side[rn.i][32 + lane] = de;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(rn.at(n_aux));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rn.at(n_aux));
+      }
+    } else {
+      for (; ok && it.next();) {
+        const size_t g0 = (size_t)it.bk * p.N;
+        const float over = -1.f / p.scale;
+        for (int j0 = 0; j0 < it.n && ok; j0 += kAhead) {
+          // loads of several tiles at once: one by one, their latency would
+          // bound the kernel
+          float l[kAhead][2], de[kAhead][2];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = (it.n0 + j0 + u) * 64 + 32 * i + lane;
+              const bool on = j0 + u < it.n && row < p.N;  // rows past the end: probability zero
+              l[u][i] = on ? p.lse_in[g0 + row] : -INFINITY;
+              de[u][i] = on ? p.delta[g0 + row] : 0.f;
+            }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            if (j0 + u >= it.n || !wait(rn.at(n_empty), rn.parity ^ 1u)) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 32 * i + lane, at = (r >> 3) * 256 + (r & 7) * 16;
+              const float nl = l[u][i] == -INFINITY ? -INFINITY : l[u][i] * over;  // no keys: probability zero
+              *reinterpret_cast<uint2*>(S.side.terms[rn.i][0] + at) = three_terms(nl);
+              *reinterpret_cast<uint2*>(S.side.terms[rn.i][1] + at) = three_terms(-de[u][i]);
+            }
+            fence_proxy_async_smem();  // generic writes -> MMA operand reads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rn.at(n_aux));
+            rn.next();
+          }
+        }
       }
     }
   } else if (warp >= C::kEpi) {
@@ -420,14 +485,14 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     const uint32_t tacc = tbase + ((uint32_t)(q4 * 32) << 16) + C::kColAcc;
     int last_b = -1;
     bool one = false;
-    Ring<2> ra;
+    Ring<C::kBufs> ra;
     Ring<C::kSums> rx;
     uint32_t par = 0;  // of acc_full and staged: the item's
     for (; ok && it.next(); ) {
       const int row = it.r0 + r;
       const bool new_b = it.b != last_b;
       last_b = it.b;
-      if (kDq) {
+      if constexpr (kDq) {
         const bool valid = row < p.N;
         const size_t grow = (size_t)it.bk * p.N + row;
         const size_t rows = (size_t)p.B * p.H * p.N;
@@ -448,11 +513,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           continue;
         }
         if (!wait(rx.at(x_full), rx.parity)) break;
-        const float c0 = S.q.c[rx.i][r];
+        const float c0 = S.side.c[rx.i][r];
         float sp = 0.f, sd = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float2 x = S.q.sums[rx.i][g][r];
+          const float2 x = S.side.sums[rx.i][g][r];
           sp += x.x;
           sd += x.y;
         }
@@ -575,7 +640,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     float lse_next = 0.f;
     if (kDq) lse_next = p.lse_in[it.peek(r)];
     for (; ok && it.next();) {
-      if (kDq) {
+      if constexpr (kDq) {
         const float lse = lse_next;
         lse_next = p.lse_in[it.peek(r)];
         if (it.n == 0) continue;
@@ -588,7 +653,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           if (clean && !wait(rn.at(n_aux), rn.parity)) break;
           if (!have_c && j > 0) {  // another group has the item's first tile
             if (!wait(rx.at(c_full), rx.parity)) break;
-            const float c0 = S.q.c[rx.i][r];
+            const float c0 = S.side.c[rx.i][r];
             c2 = f2_make(c0, c0);
             have_c = true;
           }
@@ -619,7 +684,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             c2 = f2_make(c0, c0);
             have_c = true;
             if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
-            S.q.c[rx.i][r] = c0;
+            S.side.c[rx.i][r] = c0;
             mbar_arrive(rx.at(c_full));
           }
 #pragma unroll 1
@@ -653,16 +718,13 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         j -= it.n;
         if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
         const float2 l2 = f2_split(ls), d2 = f2_split(ds);
-        S.q.sums[rx.i][g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
+        S.side.sums[rx.i][g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
         mbar_arrive(rx.at(x_full));
         rx.next();
       } else {
-        for (; j < it.n; j += NG, rn.next(NG), turn ^= 1u) {
-          const bool x_seen = look(rn.at(n_aux), rn.parity), s_seen = look(s_full + 8 * g, turn);
-          if (!finish(x_seen, rn.at(n_aux), rn.parity)) break;
-          if (!finish(s_seen, s_full + 8 * g, turn)) break;
+        for (; j < it.n; j += NG, turn ^= 1u) {
+          if (!wait(s_full + 8 * g, turn)) break;
           tc_fence_after();
-          const float2* side = S.side[rn.i];
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {  // 16 queries
             float x[16], d[16];
@@ -671,21 +733,12 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             tmem_wait_ld();
             uint32_t pk[8], dk[8];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float4 nl = *reinterpret_cast<const float4*>(side + 8 * c + i);
-              const float4 de = *reinterpret_cast<const float4*>(side + 32 + 8 * c + i);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int e = 2 * (i + u);
-                const float2 t = f2_split(f2_fma(f2_make(x[e], x[e + 1]), sc2x2,
-                                                 u ? f2_make(nl.z, nl.w) : f2_make(nl.x, nl.y)));
-                const float p0 = ex2_approx(t.x), p1 = ex2_approx(t.y);
-                const float2 q = f2_split(f2_mul(f2_make(p0, p1),
-                                                 f2_sub(f2_make(d[e], d[e + 1]),
-                                                        u ? f2_make(de.z, de.w) : f2_make(de.x, de.y))));
-                pk[i + u] = pack_bf16(p0, p1);
-                dk[i + u] = pack_bf16(q.x, q.y);
-              }
+            for (int i = 0; i < 8; ++i) {
+              const float2 e = f2_split(f2_mul(f2_make(x[2 * i], x[2 * i + 1]), sc2x2));
+              const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+              const float2 q = f2_split(f2_mul(f2_make(p0, p1), f2_make(d[2 * i], d[2 * i + 1])));
+              pk[i] = pack_bf16(p0, p1);
+              dk[i] = pack_bf16(q.x, q.y);
             }
             tmem_st8u(ts + 8 * c, pk);
             tmem_st8u(ts + 64 + 8 * c, dk);
@@ -779,12 +832,13 @@ cross_dkv_join(CrossParams p) {
 template <int D, bool kDq>
 cudaError_t launch_pass(const CrossParams& p, const CUtensorMap* a, const CUtensorMap* n, const CUtensorMap& dq,
                         int grid, cudaStream_t s) {
-  constexpr size_t smem = Cfg<D>::kEnd + sizeof(Shared<Cfg<D>>);
+  using C = Cfg<D, kDq>;
+  constexpr size_t smem = C::kEnd + sizeof(Shared<C>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   cudaError_t e =
       cudaFuncSetAttribute(cross_bwd_tc_kernel<D, kDq>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cross_bwd_tc_kernel<D, kDq><<<grid, Cfg<D>::kThreads, smem, s>>>(a[0], a[1], n[0], n[1], dq, p);
+  cross_bwd_tc_kernel<D, kDq><<<grid, C::kThreads, smem, s>>>(a[0], a[1], n[0], n[1], dq, p);
   return cudaGetLastError();
 }
 

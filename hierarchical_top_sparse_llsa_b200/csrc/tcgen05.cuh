@@ -238,6 +238,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
+// The same without a swizzle, K-major: 8 rows x 16 bytes lie together, lbo
+// bytes on the next 16 bytes of the rows, sbo bytes on the next 8 rows.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46;
+}
+
 // Instruction descriptor of kind::f16 with bf16 A and B, f32 accumulation,
 // M x N tile; b_mn_major / a_mn_major select MN-major operands (otherwise
 // K-major).
