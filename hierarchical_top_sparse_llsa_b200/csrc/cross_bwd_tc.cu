@@ -56,7 +56,8 @@ struct Sizes {
   static constexpr int kStages = (D == 64) ? 3 : 2;
   static constexpr int kEpi = kStages * 4;  // first epilogue warp
   static constexpr int kLoad = kEpi + 4, kMma = kLoad + 1, kProd = kMma + 1, kAux = kProd + 1;
-  static constexpr int kThreads = (kAux + 1) * 32;
+  static constexpr int kAuxWarps = (D == 64) ? 4 : 2;  // each has every kAuxWarps-th tile
+  static constexpr int kThreads = (kAux + kAuxWarps) * 32;
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
   static constexpr int kSlots = (D == 64) ? 6 : 3;
@@ -72,9 +73,6 @@ struct Shared {
   uint32_t bits[C::kSlots][2];  // first pass: keys seen, by slot
   typename C::Side side;
 };
-
-// Tiles whose lse and Delta the second pass's aux warp loads at once.
-constexpr int kAhead = 4;
 
 // First pass: of the rows of an item (two of them where there is room).
 template <int kSums, int kStages>
@@ -335,25 +333,33 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     Ring<NS> rn, pn;  // tiles; and the tiles NG before, whose stages these take
     Ring<NG> rs;
     int fresh = NG;   // stages not used yet
+    // of the next tile: whether it has been loaded, and the products that read
+    // its stage are done
+    bool n_seen = false, e_seen = false;
     for (; ok && it.next();) {
       const int n = uniform(it.n);
       if (n == 0) continue;
       if (!wait(ra.at(a_full), ra.parity)) break;
       const uint64_t a1 = desc_at(kmaj, abuf(ra.i));
       for (int j = 0; j < n; ++j) {
-        const bool n_seen = look(rn.at(n_full), rn.parity), x_seen = kDq || look(rn.at(n_aux), rn.parity);
-        if (fresh > 0) {
-          --fresh;
-        } else {  // the products that read the stage are done
-          if (!wait(pn.at(n_empty), pn.parity)) break;
-          pn.next();
+        if (!__all_sync(0xffffffffu, n_seen)) {
+          if (!wait(rn.at(n_full), rn.parity)) break;
+          if (!kDq && !wait(rn.at(n_aux), rn.parity)) break;
         }
-        if (!finish(n_seen, rn.at(n_full), rn.parity)) break;
-        if (!kDq && !finish(x_seen, rn.at(n_aux), rn.parity)) break;
+        if (fresh == 0) {
+          if (!finish(e_seen, pn.at(n_empty), pn.parity)) break;
+          pn.next();
+        } else {
+          --fresh;
+        }
+        const uint32_t slot = rn.i;
+        rn.next();
+        n_seen = look(rn.at(n_full), rn.parity) && (kDq || look(rn.at(n_aux), rn.parity));
+        e_seen = look(pn.at(n_empty), pn.parity);
         tc_fence_after();
         const uint32_t ts = tbase + rs.i * 128;
         const uint32_t idesc_s = idesc_bf16_f32(128, 16 * (kDq ? uniform(it.steps(j)) : 4), 0, 0);
-        const uint64_t n1 = desc_at(kmaj, nslot(rn.i));
+        const uint64_t n1 = desc_at(kmaj, nslot(slot));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
@@ -364,10 +370,9 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           const uint64_t x = smem_desc_plain(smem_u32(S.side.ones), 128, 256);
 #pragma unroll
           for (int w = 0; w < 2; ++w)
-            tc_mma_f16_by(lead, ts + 64 * w, x, desc_at(x, 4096 + rn.i * 4096 + w * 2048), idesc_s, 1);
+            tc_mma_f16_by(lead, ts + 64 * w, x, desc_at(x, 4096 + slot * 4096 + w * 2048), idesc_s, 1);
         }
         tc_commit_by(lead, rs.at(s_full));
-        rn.next();
         rs.next();
       }
       if (!ok) break;
@@ -414,11 +419,14 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     }
     tc_commit_by(lead, smem_u32(&S.done));
     if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
-  } else if (warp == C::kAux) {
+  } else if (warp >= C::kAux) {
+    constexpr int NA = C::kAuxWarps;
     Ring<NS> rn;
+    rn.next(warp - C::kAux);
+    int j = warp - C::kAux;  // this warp's next tile of the item
     if constexpr (kDq) {
-      for (; ok && clean && it.next();) {
-        for (int j = 0; j < it.n && ok; ++j, rn.next()) {
+      for (; ok && clean && it.next(); j -= it.n) {
+        for (; j < it.n; j += NA, rn.next(NA)) {
           uint32_t word[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -443,40 +451,46 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           __syncwarp();
           if (lane == 0) mbar_arrive(rn.at(n_aux));
         }
+        if (!ok) break;
       }
     } else {
-      for (; ok && it.next();) {
+      const float over = -1.f / p.scale;
+      for (; ok && it.next(); j -= it.n) {
         const size_t g0 = (size_t)it.bk * p.N;
-        const float over = -1.f / p.scale;
-        for (int j0 = 0; j0 < it.n && ok; j0 += kAhead) {
-          // loads of several tiles at once: one by one, their latency would
-          // bound the kernel
-          float l[kAhead][2], de[kAhead][2];
+        float l[2], de[2];
+        auto load = [&]() {
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = (it.n0 + j0 + u) * 64 + 32 * i + lane;
-              const bool on = j0 + u < it.n && row < p.N;  // rows past the end: probability zero
-              l[u][i] = on ? p.lse_in[g0 + row] : -INFINITY;
-              de[u][i] = on ? p.delta[g0 + row] : 0.f;
-            }
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            if (j0 + u >= it.n || !wait(rn.at(n_empty), rn.parity ^ 1u)) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = 32 * i + lane, at = (r >> 3) * 256 + (r & 7) * 16;
-              const float nl = l[u][i] == -INFINITY ? -INFINITY : l[u][i] * over;  // no keys: probability zero
-              *reinterpret_cast<uint2*>(S.side.terms[rn.i][0] + at) = three_terms(nl);
-              *reinterpret_cast<uint2*>(S.side.terms[rn.i][1] + at) = three_terms(-de[u][i]);
-            }
-            fence_proxy_async_smem();  // generic writes -> MMA operand reads
-            __syncwarp();
-            if (lane == 0) mbar_arrive(rn.at(n_aux));
-            rn.next();
+          for (int i = 0; i < 2; ++i) {
+            const int row = (it.n0 + j) * 64 + 32 * i + lane;
+            const bool on = j < it.n && row < p.N;  // rows past the end: probability zero
+            l[i] = on ? p.lse_in[g0 + row] : -INFINITY;
+            de[i] = on ? p.delta[g0 + row] : 0.f;
           }
+        };
+        load();
+        while (j < it.n) {
+          uint2 x[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            x[0][i] = three_terms(l[i] == -INFINITY ? -INFINITY : l[i] * over);  // no keys: probability zero
+            x[1][i] = three_terms(-de[i]);
+          }
+          if (!wait(rn.at(n_empty), rn.parity ^ 1u)) break;
+          j += NA;
+          load();
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 32 * i + lane;
+              *reinterpret_cast<uint2*>(S.side.terms[rn.i][w] + (r >> 3) * 256 + (r & 7) * 16) = x[w][i];
+            }
+          fence_proxy_async_smem();  // generic writes -> MMA operand reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(rn.at(n_aux));
+          rn.next(NA);
         }
+        if (!ok) break;
       }
     }
   } else if (warp >= C::kEpi) {
