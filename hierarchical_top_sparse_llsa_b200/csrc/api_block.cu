@@ -152,7 +152,7 @@ inline int rows_per_key_head(const llsa_cross_desc* d) { return d->H / d->Hkv * 
 CrossWs cross_fwd_ws(const llsa_cross_desc* d) {
   CrossWs w;
   const long long BH = (long long)d->B * d->Hkv;
-  w.plan = d->dtype == LLSA_BF16 ? cross_tc_fwd_plan(BH, rows_per_key_head(d), d->S)
+  w.plan = d->dtype == LLSA_BF16 ? cross_tc_fwd_plan(BH, rows_per_key_head(d), d->S, d->D)
                                  : cross_simt_fwd_plan(BH, rows_per_key_head(d), d->S);
   const size_t rows = (size_t)d->B * d->H * d->N;
   if (w.plan.nks > 1) {
@@ -381,7 +381,7 @@ int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, const void* 
     CUtensorMap qo[2], kv[2];
     const void* const rows_of[2] = {q, o};
     st = make_query_maps(qo, desc, rows_of, 2, 128);
-    if (st == LLSA_OK) st = make_key_maps(kv, desc, k, v, q, 128);
+    if (st == LLSA_OK) st = make_key_maps(kv, desc, k, v, q, desc->D == 64 ? 64 : 128);
     if (st != LLSA_OK) return st;
     const CUtensorMap maps[4] = {qo[0], kv[0], kv[1], qo[1]};
     err = launch_cross_fwd_tc(p, maps, s);

@@ -69,12 +69,13 @@ struct CrossPlan {
 };
 CrossPlan cross_simt_fwd_plan(long long BH, int N, int S);
 CrossPlan cross_simt_bwd_plan(long long BH, int N, int S);
-CrossPlan cross_tc_fwd_plan(long long BH, int N, int S);
+CrossPlan cross_tc_fwd_plan(long long BH, int N, int S, int D);
 CrossPlan cross_tc_bwd_plan(long long BH, int N, int S);
 
 constexpr int kCrossSms = 148;  // SMs of a B200
 
-// maps: Q, K, V, O as 3D [B H, rows, D] bf16, box 128 rows x 64 columns, 128-byte swizzle
+// maps: Q, K, V, O as 3D [B H, rows, D] bf16, 128-byte swizzle, boxes of 64
+// columns and 128 rows (K, V at D = 64: 64 rows)
 cudaError_t launch_cross_fwd_tc(const CrossParams& p, const CUtensorMap* maps, cudaStream_t s);
 // q128, kv64, kv128, q64: (Q, dO) or (K, V) as above, boxes of 128 or 64 rows; q128[2]: dQ
 cudaError_t launch_cross_bwd_tc(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,

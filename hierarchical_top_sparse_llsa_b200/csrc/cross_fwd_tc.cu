@@ -5,25 +5,28 @@
 // keys.
 //
 // The query heads of a key head are neighbours in memory, so their queries
-// are one run of R rows against the same keys.  A work item is 256 of these
-// rows (two tiles of 128, the M of an MMA) against a range of key tiles of
-// 128; a persistent CTA per SM walks a contiguous range of items:
-//   warps 0-3, 4-7  softmax of the two query tiles, one thread per row;
-//   warp 8          TMA loads: Q tiles into a ring of slots, K and V tiles
-//                   into another.  Key tiles that fit in the ring are loaded
-//                   once and stay for all items of the same keys;
-//   warp 9          issues the MMAs: S_w = Q_w K^T into tensor
-//                   memory, and O_w += P_w V with P_w read from tensor memory
-//                   (over S_w, which the softmax has read);
-//   warp 10         with lengths or a mask: the bits of the keys seen in each
-//                   tile, and zeros over the V rows that are not seen (their
-//                   probability is zero, and zero times NaN is NaN);
-//   warp 11         TMA stores of the finished O tiles, staged over their Q.
-// The two query tiles take turns: the tensor cores work on one while the
-// exponentials of the other are computed, which bound the kernel (one per
-// score; 16 a clock and SM).  The next item's first S is issued before this
-// item's epilogue.  Few rows: the keys are cut into ranges, each a work item
-// of its own, whose fp32 parts are joined by another kernel.
+// are one run of R rows against the same keys.  A work item is kNq tiles of
+// 128 of these rows (the M of an MMA) against a range of key tiles; a
+// persistent CTA per SM walks a contiguous range of items.  Warps:
+//   four per query tile: its softmax, one thread per row;
+//   load   TMA loads: Q tiles into a ring of slots, K and V tiles into
+//          another.  Key tiles that fit in the ring are loaded once and stay
+//          for all items of the same keys;
+//   mma    (one for every two query tiles) issues S_w = Q_w K^T into tensor
+//          memory, and O_w += P_w V with P_w read from tensor memory (over
+//          S_w, which the softmax has read);
+//   clean  with lengths or a mask: the bits of the keys seen in each tile,
+//          and zeros over the V rows that are not seen (their probability is
+//          zero, and zero times NaN is NaN);
+//   store  TMA stores of the finished O tiles, staged over their Q.
+// The query tiles take turns: the tensor cores work on some while the
+// exponentials of the others are computed, which bound the kernel (one per
+// score; 16 a clock and SM).  At D = 64 four query tiles are in flight, each
+// against 64 keys at a time; at D = 128 tensor memory holds two, and they take
+// 128 keys, an N that the tensor cores run at full rate.  The next item's
+// first S is issued before this item's epilogue.  Few rows: the keys are cut
+// into ranges, each a work item of its own, whose fp32 parts are joined by
+// another kernel.
 // P is rounded to bf16 for the product (the exact running maximum is kept, so
 // a row's largest probability is 1 and rounds exactly); m, l and O are fp32.
 // Every wait is bounded; a time-out is reported as LLSA_DEV_TIMEOUT.
@@ -37,43 +40,49 @@ namespace llsa {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClean = 10, kWarpStore = 11;
-
 template <int D>
 struct Cfg {
-  static constexpr int kTile = 128 * D * 2;             // a Q, K or V tile
-  static constexpr int kQ = (D == 64) ? 4 : 3;          // Q slots
-  static constexpr int kKv = (D == 64) ? 8 : 4;         // K and V slots
-  static constexpr int kEnd = (kQ + kKv) * kTile;
-  static constexpr uint32_t kColO = 256;                // S_0 | S_1 | O_0 | O_1
+  static constexpr int kNq = (D == 64) ? 4 : 2;         // query tiles of an item
+  static constexpr int kKeys = (D == 64) ? 64 : 128;    // keys of a tile
+  static constexpr int kMmaWarps = kNq / 2;
+  static constexpr int kLoad = kNq * 4, kMma = kLoad + 1, kClean = kMma + kMmaWarps, kStore = kClean + 1;
+  static constexpr int kThreads = (kStore + 1) * 32;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int kKvTile = kKeys * D * 2;
+  static constexpr int kQ = (D == 64) ? 8 : 3;          // Q slots
+  static constexpr int kKv = (D == 64) ? 12 : 4;        // K and V slots
+  static constexpr int kOffKv = kQ * kQTile;
+  static constexpr int kEnd = kOffKv + kKv * kKvTile;
+  static constexpr int kColO = 256;                     // S of each tile, O of each tile
 };
 
+template <typename C>
 struct Shared {
-  uint64_t q_full[4], q_empty[4], kv_full[8], kv_empty[8], kv_clean[8];
-  uint64_t s_full[2], p_full[2], o_full[2], o_staged[2], done;
-  uint32_t bits[8][4];  // keys seen, by V slot
+  uint64_t q_full[C::kQ], q_empty[C::kQ], kv_full[C::kKv], kv_empty[C::kKv], kv_clean[C::kKv];
+  uint64_t s_full[C::kNq], p_full[C::kNq], o_full[C::kNq], o_staged[C::kNq], done;
+  uint32_t bits[C::kKv][C::kKeys / 32];  // keys seen, by V slot
   uint32_t tmem_base;
 };
 
-// The items of a CTA, in order: 256 query rows of one key head against one
-// range of its key tiles.  Every warp role walks them by itself; rows are
+// The items of a CTA, in order: kNq * 128 query rows of one key head against
+// one range of its key tiles.  Every warp role walks them by itself; rows are
 // innermost, so items of the same keys follow one another (a run).
+template <typename C>
 struct FwdItems {
   const CrossParams& p;
-  int i, end, nt, cap;
+  int i, end, nt;
   int R;                       // query rows of a key head
   size_t rows;                 // and of all of them
   int bk, b, split, tile, r0, len;  // the item: key head, batch entry, key range, rows, keys seen at the front
   int kt0, nkt;                // its key tiles
-  bool act1;                   // whether its second tile of 128 rows has any
+  int nact;                    // its query tiles that have rows
   bool first, new_run, last_of_run;
   bool resident;               // its key tiles fit in the ring: loaded once for the run
 
-  __device__ __forceinline__ FwdItems(const CrossParams& p_, int cap_) : p(p_), cap(cap_), b(-1) {
+  __device__ __forceinline__ FwdItems(const CrossParams& p_) : p(p_), b(-1) {
     R = p.N;
     rows = (size_t)p.B * p.H * R;
-    nt = (R + 255) / 256;
+    nt = (R + C::kNq * 128 - 1) / (C::kNq * 128);
     i = (int)p.runs.begin(blockIdx.x) - 1;
     end = (int)p.runs.begin(blockIdx.x + 1);
     const int run = (i + 1) / nt;
@@ -91,13 +100,13 @@ struct FwdItems {
       len = cross_len(p, b);
     }
     kt0 = 0;
-    nkt = (len + 127) / 128;
+    nkt = (len + C::kKeys - 1) / C::kKeys;
     if (p.nks > 1) {  // the first nkt % nks ranges are longer by one
       const int each = nkt / p.nks, more = nkt - each * p.nks;
       kt0 = each * split + min(split, more);
       nkt = each + (split < more);
     }
-    resident = nkt <= cap;
+    resident = 2 * nkt <= C::kKv;
   }
   __device__ __forceinline__ bool next() {
     if (i + 1 >= end) return false;
@@ -114,224 +123,236 @@ struct FwdItems {
       range();
     }
     last_of_run = tile == nt - 1 || i + 1 == end;
-    r0 = tile * 256;
-    act1 = r0 + 128 < R;
+    r0 = tile * C::kNq * 128;
+    nact = min(C::kNq, (R - r0 + 127) / 128);
     return true;
   }
+  // whether the item's keys are loaded for it
+  __device__ __forceinline__ bool loads() const { return !resident || new_run; }
   // 16-key steps of key tile j of the item
   __device__ __forceinline__ int steps(int j) const {
-    const int n = len - (kt0 + j) * 128;
-    return n >= 128 ? 8 : (n + 15) >> 4;
+    const int n = len - (kt0 + j) * C::kKeys;
+    return n >= C::kKeys ? C::kKeys / 16 : (n + 15) >> 4;
   }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, CrossParams p) {
   using C = Cfg<D>;
   constexpr int H = D / 64;  // 64-column halves of a tile
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  Shared& S = *reinterpret_cast<Shared*>(sm + C::kEnd);
+  constexpr int kKvHalf = C::kKeys * 128;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  Shared<C>& S = *reinterpret_cast<Shared<C>*>(sm + C::kEnd);
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const bool clean = p.mask != nullptr || p.kv_len != nullptr;
   bool ok = true;
 
-  if (warp == kWarpMma) {
+  if (warp == C::kMma) {
     tmem_alloc(smem_u32(&S.tmem_base), 512);
     tmem_relinquish();
   } else if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < C::kQ; ++i) {
       mbar_init(smem_u32(&S.q_full[i]), 1);
       mbar_init(smem_u32(&S.q_empty[i]), 1);
     }
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < C::kKv; ++i) {
       mbar_init(smem_u32(&S.kv_full[i]), 1);
-      mbar_init(smem_u32(&S.kv_empty[i]), 1);
+      mbar_init(smem_u32(&S.kv_empty[i]), C::kMmaWarps);
       mbar_init(smem_u32(&S.kv_clean[i]), 1);
     }
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < C::kNq; ++w) {
       mbar_init(smem_u32(&S.s_full[w]), 1);
       mbar_init(smem_u32(&S.p_full[w]), 128);
       mbar_init(smem_u32(&S.o_full[w]), 1);
       mbar_init(smem_u32(&S.o_staged[w]), 128);
     }
-    mbar_init(smem_u32(&S.done), 1);
+    mbar_init(smem_u32(&S.done), C::kMmaWarps);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = uniform(S.tmem_base);
-  auto qslot = [&](int t) { return base + (uint32_t)(t % C::kQ) * C::kTile; };
-  auto kvslot = [&](int f) { return base + (uint32_t)(C::kQ + f % C::kKv) * C::kTile; };
-  FwdItems it(p, C::kKv / 2);
+  auto qslot = [&](uint32_t i) { return base + i * C::kQTile; };
+  auto kvslot = [&](uint32_t i) { return base + C::kOffKv + i * C::kKvTile; };
+  const uint32_t q_full = smem_u32(S.q_full), q_empty = smem_u32(S.q_empty), kv_full = smem_u32(S.kv_full),
+                 kv_empty = smem_u32(S.kv_empty), kv_clean = smem_u32(S.kv_clean), s_full = smem_u32(S.s_full),
+                 p_full = smem_u32(S.p_full), o_full = smem_u32(S.o_full), o_staged = smem_u32(S.o_staged);
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+  FwdItems<C> it(p);
 
-  if (warp == kWarpLoad) {
+  if (warp == C::kLoad) {
     if (lane == 0) {
-      int t = 0, f = 0;  // Q tiles and K/V tiles loaded so far
-      auto load = [&](uint32_t dst, const CUtensorMap* map, int row, int bk, uint64_t* bar) {
-        mbar_arrive_expect_tx(smem_u32(bar), C::kTile);
+      Ring<C::kQ> rq;
+      Ring<C::kKv> rk;
+      // a slot's first round waits for the phase before the first, which is over
+      auto load = [&](uint32_t dst, uint32_t half, const CUtensorMap* map, int row, uint32_t full, uint32_t bytes) {
+        mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
-        for (int h = 0; h < H; ++h) tma_load_3d(dst + h * 16384, map, 64 * h, row, bk, smem_u32(bar));
+        for (int h = 0; h < H; ++h) tma_load_3d(dst + h * half, map, 64 * h, row, it.bk, full);
       };
       auto load_q = [&](int w) {
-        if (t >= C::kQ) ok = mbar_wait(smem_u32(&S.q_empty[t % C::kQ]), (uint32_t)((t / C::kQ - 1) & 1));
+        if (ok) ok = mbar_wait(rq.at(q_empty), rq.parity ^ 1u);
         if (!ok) return;
-        load(qslot(t), &tq, it.r0 + 128 * w, it.bk, &S.q_full[t % C::kQ]);
-        ++t;
+        load(qslot(rq.i), 16384, &tq, it.r0 + 128 * w, rq.at(q_full), C::kQTile);
+        rq.next();
+      };
+      auto load_kv = [&](const CUtensorMap* map, int j) {
+        if (ok) ok = mbar_wait(rk.at(kv_empty), rk.parity ^ 1u);
+        if (!ok) return;
+        load(kvslot(rk.i), kKvHalf, map, (it.kt0 + j) * C::kKeys, rk.at(kv_full), C::kKvTile);
+        rk.next();
       };
       for (; ok && it.next();) {
         if (it.nkt == 0) continue;
-        // the second Q tile goes before the keys that have to wait for it to
-        // be used: every step needs both
+        const int n = it.loads() ? it.nkt : 0;
         load_q(0);
-        const int nkv = (!it.resident || it.new_run) ? 2 * it.nkt : 0;
-        for (int j = 0; j < nkv && ok; ++j) {
-          if (j == 2 && it.act1) load_q(1);
-          if (f >= C::kKv && ok)
-            ok = mbar_wait(smem_u32(&S.kv_empty[f % C::kKv]), (uint32_t)((f / C::kKv - 1) & 1));
-          if (!ok) break;
-          load(kvslot(f), (j & 1) ? &tv : &tk, (it.kt0 + j / 2) * 128, it.bk, &S.kv_full[f % C::kKv]);
-          ++f;
+        if (n > 0) load_kv(&tk, 0);
+        for (int w = 1; w < it.nact; ++w) load_q(w);
+        if (n > 0) load_kv(&tv, 0);
+        for (int j = 1; j < n && ok; ++j) {
+          load_kv(&tk, j);
+          load_kv(&tv, j);
         }
-        if (ok && it.act1 && nkv <= 2) load_q(1);
       }
-      // no copy may still be landing when the CTA exits
-      for (int i = t > C::kQ ? t - C::kQ : 0; i < t; ++i)
-        if (!mbar_wait(smem_u32(&S.q_full[i % C::kQ]), (uint32_t)((i / C::kQ) & 1))) ok = false;
-      for (int i = f > C::kKv ? f - C::kKv : 0; i < f; ++i)
-        if (!mbar_wait(smem_u32(&S.kv_full[i % C::kKv]), (uint32_t)((i / C::kKv) & 1))) ok = false;
+      // no copy may still be landing when the CTA exits: of every slot, the
+      // last round that was begun
+      for (int i = 0; i < C::kQ; ++i, rq.next())
+        if (!mbar_wait(rq.at(q_full), rq.parity ^ 1u)) ok = false;
+      for (int i = 0; i < C::kKv; ++i, rk.next())
+        if (!mbar_wait(rk.at(kv_full), rk.parity ^ 1u)) ok = false;
     }
-  } else if (warp == kWarpMma) {
-    // the whole warp walks; one lane issues
+  } else if (warp >= C::kMma && warp < C::kClean) {
+    // query tiles w0 and w0 + 1; the whole warp walks, one lane issues
+    const int w0 = 2 * (warp - C::kMma);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1, 0);
-    const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, 16384, 1024);
+    const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, kKvHalf, 1024);
     const uint32_t lead = elect_lane();
-    int t = 0, f = 0, frun = 0;
-    int np[2] = {0, 0};      // P tiles taken
+    Ring<C::kQ> rq;                // of the item's first query tile
+    Ring<C::kKv> run, kv, pv_at;   // the run's first tile, this step's K, the pending products' V
+    uint32_t turn[2] = {0, 0};     // parity of p_full
     bool pend[2] = {false, false};
-    int pf = 0, pnt = 0;     // the pending product's V tile and its 16-key steps
+    int pnt = 0;                   // the pending products' 16-key steps
     bool pfirst = false, plast = false, pfree = false;
-    auto wait = [&](uint64_t* bar, int phase) {
-      return ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), (uint32_t)(phase & 1)));
-    };
-    auto pv = [&](int w) {   // O_w (+)= P_w V of the previous step
-      if (!pend[w]) return;
-      pend[w] = false;
-      if (!wait(&S.kv_full[pf % C::kKv], pf / C::kKv)) return;
-      if (clean && !wait(&S.kv_clean[pf % C::kKv], pf / C::kKv)) return;
-      if (!wait(&S.p_full[w], np[w])) return;
-      ++np[w];
+    auto products = [&](int u) {   // O_w (+)= P_w V of the previous step
+      if (!pend[u]) return;
+      pend[u] = false;
+      const int w = w0 + u;
+      if (clean ? !wait(pv_at.at(kv_clean), pv_at.parity) : !wait(pv_at.at(kv_full), pv_at.parity)) return;
+      if (!wait(p_full + 8 * w, turn[u])) return;
+      turn[u] ^= 1u;
       tc_fence_after();
-      const uint64_t v = desc_at(nmaj, kvslot(pf));
+      const uint64_t v = desc_at(nmaj, kvslot(pv_at.i));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < C::kKeys / 16; ++k) {
         if (k >= pnt) break;
-        tc_mma_f16_ts_by(lead, tbase + C::kColO + w * D, tbase + w * 128 + k * 8, desc_at(v, k * 2048), idesc_pv,
+        tc_mma_f16_ts_by(lead, tbase + C::kColO + w * D, tbase + w * C::kKeys + k * 8, desc_at(v, k * 2048), idesc_pv,
                          !pfirst || k > 0);
       }
-      if (plast) tc_commit_by(lead, smem_u32(&S.o_full[w]));
+      if (plast) tc_commit_by(lead, o_full + 8 * w);
     };
     for (; ok && it.next();) {
-      const int nkt = uniform(it.nkt);
+      const int nkt = uniform(it.nkt), nact = uniform(it.nact);
       if (nkt == 0) continue;
-      const bool resident = nkt <= it.cap;
-      if (!resident || it.new_run) {
-        frun = f;
-        f += 2 * nkt;
+      const bool loads = 2 * nkt > C::kKv || it.new_run, free = 2 * nkt > C::kKv || it.last_of_run;
+      if (loads) {
+        run = kv;
+      } else {
+        kv = run;
       }
-      const int t0 = t;
-      t += it.act1 ? 2 : 1;
       for (int j = 0; j < nkt && ok; ++j) {
-        const int fk = frun + 2 * j;
         const int nt = uniform(it.steps(j));
         const uint32_t idesc_s = idesc_bf16_f32(128, 16 * nt, 0, 0);
-        const uint64_t k = desc_at(kmaj, kvslot(fk));
-        if (!wait(&S.kv_full[fk % C::kKv], fk / C::kKv)) break;
+        const uint64_t k = desc_at(kmaj, kvslot(kv.i));
+        if (!wait(kv.at(kv_full), kv.parity)) break;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (ok) pv(w);
-          if (!ok || (w == 1 && !it.act1)) continue;
-          const int tw = t0 + w;
-          if (j == 0 && !wait(&S.q_full[tw % C::kQ], tw / C::kQ)) continue;
+        for (int u = 0; u < 2; ++u) {
+          if (ok) products(u);
+          const int w = w0 + u;
+          if (!ok || w >= nact) continue;
+          Ring<C::kQ> at = rq;
+          at.next(w);
+          if (j == 0 && !wait(at.at(q_full), at.parity)) continue;
           tc_fence_after();
-          const uint64_t q = desc_at(kmaj, qslot(tw));
+          const uint64_t q = desc_at(kmaj, qslot(at.i));
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            tc_mma_f16_by(lead, tbase + w * 128, desc_at(q, (ks >> 2) * 16384 + (ks & 3) * 32),
-                          desc_at(k, (ks >> 2) * 16384 + (ks & 3) * 32), idesc_s, ks > 0);
-          tc_commit_by(lead, smem_u32(&S.s_full[w]));
-          pend[w] = true;
+            tc_mma_f16_by(lead, tbase + w * C::kKeys, desc_at(q, (ks >> 2) * 16384 + (ks & 3) * 32),
+                          desc_at(k, (ks >> 2) * kKvHalf + (ks & 3) * 32), idesc_s, ks > 0);
+          tc_commit_by(lead, s_full + 8 * w);
+          pend[u] = true;
         }
         if (!ok) break;
-        if (pfree) tc_commit_by(lead, smem_u32(&S.kv_empty[pf % C::kKv]));
-        pf = fk + 1;
+        if (pfree) tc_commit_by(lead, pv_at.at(kv_empty));
+        if (free) tc_commit_by(lead, kv.at(kv_empty));
+        pv_at = kv;
+        pv_at.next();
         pnt = nt;
         pfirst = j == 0;
         plast = j == nkt - 1;
-        pfree = !resident || it.last_of_run;
-        if (pfree) tc_commit_by(lead, smem_u32(&S.kv_empty[fk % C::kKv]));
+        pfree = free;
+        kv.next(2);
       }
+      rq.next(nact);
     }
-    for (int w = 0; w < 2 && ok; ++w) pv(w);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (ok) products(u);
     // every MMA of this CTA has completed before tensor memory is freed
     tc_commit_by(lead, smem_u32(&S.done));
     if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
-  } else if (warp == kWarpClean) {
-    if (clean) {
-      int f = 0;
-      for (; ok && it.next();) {
-        if (it.nkt == 0 || (it.resident && !it.new_run)) continue;
-        for (int j = 0; j < it.nkt && ok; ++j, f += 2) {
-          const int slot = (f + 1) % C::kKv;
-          const int k0 = (it.kt0 + j) * 128;
-          uint32_t word[4];
+  } else if (warp == C::kClean) {
+    Ring<C::kKv> rv;  // of V
+    rv.next();
+    for (; ok && clean && it.next();) {
+      if (!it.loads()) continue;
+      for (int j = 0; j < it.nkt; ++j, rv.next(2)) {
+        const int k0 = (it.kt0 + j) * C::kKeys;
+        uint32_t word[C::kKeys / 32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = k0 + 32 * c + lane;
-            const bool on = key < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + key] != 0);
-            word[c] = __ballot_sync(0xffffffffu, on);
-          }
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.kv_full[slot]), (uint32_t)(((f + 1) / C::kKv) & 1)));
-          if (!ok) break;
-          const int rows = 16 * it.steps(j);
-          unsigned char* v = sm + (kvslot(f + 1) - base);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (lane == 0) S.bits[slot][c] = word[c];
-            for (uint32_t off = ~word[c]; off != 0u; off &= off - 1) {  // one row at a time, 16 bytes a lane
-              const int r = 32 * c + __ffs(off) - 1;
-              if (r >= rows) break;
-              if (lane < D / 8)
-                *reinterpret_cast<uint4*>(v + (lane >> 3) * 16384 + sw128(r, lane & 7)) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          fence_proxy_async_smem();  // generic writes -> MMA operand reads
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&S.kv_clean[slot]));
+        for (int c = 0; c < C::kKeys / 32; ++c) {
+          const int key = k0 + 32 * c + lane;
+          const bool on = key < it.len && (p.mask == nullptr || p.mask[(size_t)it.b * p.S + key] != 0);
+          word[c] = __ballot_sync(0xffffffffu, on);
         }
+        if (!wait(rv.at(kv_full), rv.parity)) break;
+        const int rows = 16 * it.steps(j);
+        unsigned char* v = sm + (kvslot(rv.i) - base);
+#pragma unroll
+        for (int c = 0; c < C::kKeys / 32; ++c) {
+          if (lane == 0) S.bits[rv.i][c] = word[c];
+          for (uint32_t off = ~word[c]; off != 0u; off &= off - 1) {  // one row at a time, 16 bytes a lane
+            const int r = 32 * c + __ffs(off) - 1;
+            if (r >= rows) break;
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(v + (lane >> 3) * kKvHalf + sw128(r, lane & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();  // generic writes -> MMA operand reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rv.at(kv_clean));
       }
     }
-  } else if (warp == kWarpStore) {
+  } else if (warp == C::kStore) {
     if (lane == 0) {
-      int t = 0, n[2] = {0, 0};
+      Ring<C::kQ> rq;
+      uint32_t turn = 0;  // parities of o_staged, a bit each
       for (; ok && it.next();) {
         if (it.nkt == 0) continue;
-        for (int w = 0; w < (it.act1 ? 2 : 1) && ok; ++w, ++t) {
-          ok = mbar_wait(smem_u32(&S.o_staged[w]), (uint32_t)(n[w] & 1));
+        for (int w = 0; w < it.nact; ++w, rq.next()) {
+          ok = mbar_wait(o_staged + 8 * w, (turn >> w) & 1u);
           if (!ok) break;
-          ++n[w];
+          turn ^= 1u << w;
           if (p.nks == 1) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) tma_store_3d(&to, 64 * h, it.r0 + 128 * w, it.bk, qslot(t) + h * 16384);
+            for (int h = 0; h < H; ++h) tma_store_3d(&to, 64 * h, it.r0 + 128 * w, it.bk, qslot(rq.i) + h * 16384);
             bulk_commit_group();
             bulk_wait_read_all();
           }
-          mbar_arrive(smem_u32(&S.q_empty[t % C::kQ]));
+          mbar_arrive(rq.at(q_empty));
         }
       }
       bulk_wait_all();
@@ -341,10 +362,13 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     const int w = warp >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t trow = tbase + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t ts = trow + (uint32_t)w * 128, tO = trow + C::kColO + (uint32_t)w * D;
+    const uint32_t ts = trow + (uint32_t)(w * C::kKeys), tO = trow + C::kColO + (uint32_t)w * D;
     const float sc2 = p.scale * kLog2e;
     const uint64_t sc2x2 = f2_make(sc2, sc2);
-    int t = 0, ns = 0, no = 0, f = 0, frun = 0;
+    Ring<C::kQ> rq;
+    Ring<C::kKv> run, rv;  // of V
+    rv.next();
+    uint32_t s_turn = 0, o_turn = 0;
     for (; ok && it.next();) {
       const int row = it.r0 + 128 * w + r;
       const size_t grow = (size_t)it.bk * it.R + row;
@@ -363,30 +387,29 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         }
         continue;
       }
-      if (!it.resident || it.new_run) {
-        frun = f;
-        f += 2 * it.nkt;
+      if (it.loads()) run = rv;
+      else rv = run;
+      Ring<C::kQ> at = rq;
+      at.next(w);
+      rq.next(it.nact);
+      if (w >= it.nact) {
+        for (int j = 0; j < it.nkt; ++j) rv.next(2);
+        continue;
       }
-      const int tw = t + w;
-      t += it.act1 ? 2 : 1;
-      if (w == 1 && !it.act1) continue;
       float m = -INFINITY;  // running maximum, in units of log2
       float l = 0.f;
-      for (int j = 0; j < it.nkt && ok; ++j, ++ns) {
+      for (int j = 0; j < it.nkt; ++j, rv.next(2)) {
         const int nch = (it.steps(j) + 1) / 2;  // chunks of 32 keys
-        const int slot = (frun + 2 * j + 1) % C::kKv;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.s_full[w]), (uint32_t)(ns & 1)));
-        if (ok && clean)
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.kv_clean[slot]),
-                                                         (uint32_t)(((frun + 2 * j + 1) / C::kKv) & 1)));
-        if (!ok) break;
+        if (!wait(s_full + 8 * w, s_turn)) break;
+        s_turn ^= 1u;
+        if (clean && !wait(rv.at(kv_clean), rv.parity)) break;
         tc_fence_after();
-        const int left = it.len - (it.kt0 + j) * 128;
-        if (clean || left < 128) {
+        const int left = it.len - (it.kt0 + j) * C::kKeys;
+        if (clean || left < C::kKeys) {
 #pragma unroll 1
           for (int c = 0; c < 2 * nch; ++c) {
-            const uint32_t bits = clean ? (S.bits[slot][c >> 1] >> (16 * (c & 1))) & 0xffffu
-                                        : (left - 16 * c >= 16 ? 0xffffu : (left <= 16 * c ? 0u : (1u << (left - 16 * c)) - 1u));
+            const uint32_t bits = clean ? (S.bits[rv.i][c >> 1] >> (16 * (c & 1))) & 0xffffu
+                                        : (1u << min(max(left - 16 * c, 0), 16)) - 1u;
             if (bits != 0xffffu) hide16(ts + 16 * c, bits, -INFINITY);
           }
         }
@@ -439,17 +462,16 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         l = l * corr + (s2.x + s2.y);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&S.p_full[w]));
+        mbar_arrive(p_full + 8 * w);
       }
       if (!ok) break;
       // ------------------------------------------------------------ epilogue
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.o_full[w]), (uint32_t)(no & 1)));
-      if (!ok) break;
-      ++no;
+      if (!wait(o_full + 8 * w, o_turn)) break;
+      o_turn ^= 1u;
       tc_fence_after();
       const bool valid = row < it.R;
       const float inv = l != 0.f ? 1.f / l : 0.f;  // 0 without keys; NaN stays NaN
-      unsigned char* stage = sm + (qslot(tw) - base);
+      unsigned char* stage = sm + (qslot(at.i) - base);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -483,7 +505,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       }
       fence_proxy_async_smem();  // generic writes -> TMA store
       tc_fence_before();
-      mbar_arrive(smem_u32(&S.o_staged[w]));
+      mbar_arrive(o_staged + 8 * w);
       if (valid) {
         if (p.nks > 1) p.part_ml[(size_t)it.split * it.rows + grow] = make_float2(m, l);
         else p.lse[grow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
@@ -494,7 +516,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
   if (!ok) report_status(p.status, LLSA_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == C::kMma) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -502,22 +524,25 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 
 template <int D>
 cudaError_t launch_typed(CrossParams p, const CUtensorMap* maps, cudaStream_t s) {
-  constexpr size_t smem = 1024 + Cfg<D>::kEnd + sizeof(Shared);
+  using C = Cfg<D>;
+  constexpr size_t smem = C::kEnd + sizeof(Shared<C>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(cross_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)p.B * p.H * p.nks * cross_tiles(p.N, 256);
+  const int64_t items = (int64_t)p.B * p.H * p.nks * cross_tiles(p.N, C::kNq * 128);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int grid = (int)(items < kCrossSms ? items : kCrossSms);
   p.runs = cross_runs(items, grid);
-  cross_fwd_tc_kernel<D><<<grid, kThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], p);
+  cross_fwd_tc_kernel<D><<<grid, C::kThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-CrossPlan cross_tc_fwd_plan(long long BH, int N, int S) {
+CrossPlan cross_tc_fwd_plan(long long BH, int N, int S, int D) {
   // cut the keys where the row tiles leave SMs without an item
-  const int64_t units = BH * cross_tiles(N, 256), kt = cross_tiles(S, 128);
+  const int rows = (D == 64 ? Cfg<64>::kNq : Cfg<128>::kNq) * 128, keys = D == 64 ? Cfg<64>::kKeys : Cfg<128>::kKeys;
+  const int64_t units = BH * cross_tiles(N, rows), kt = cross_tiles(S, keys);
   int64_t nks = kCrossSms / units;
   if (nks > kt) nks = kt;
   return {nks < 1 ? 1 : (int)nks, 1};
