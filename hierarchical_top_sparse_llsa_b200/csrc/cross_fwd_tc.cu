@@ -12,7 +12,7 @@
 //   load   TMA loads: Q tiles into a ring of slots, K and V tiles into
 //          another.  Key tiles that fit in the ring are loaded once and stay
 //          for all items of the same keys;
-//   mma    (one for every two query tiles) issues S_w = Q_w K^T into tensor
+//   mma    (one for every query tile) issues S_w = Q_w K^T into tensor
 //          memory, and O_w += P_w V with P_w read from tensor memory (over
 //          S_w, which the softmax has read);
 //   clean  with lengths or a mask: the bits of the keys seen in each tile,
@@ -44,7 +44,8 @@ template <int D>
 struct Cfg {
   static constexpr int kNq = (D == 64) ? 4 : 2;         // query tiles of an item
   static constexpr int kKeys = (D == 64) ? 64 : 128;    // keys of a tile
-  static constexpr int kMmaWarps = kNq / 2;
+  static constexpr int kPer = 2;                        // query tiles of an mma warp
+  static constexpr int kMmaWarps = kNq / kPer;
   static constexpr int kLoad = kNq * 4, kMma = kLoad + 1, kClean = kMma + kMmaWarps, kStore = kClean + 1;
   static constexpr int kThreads = (kStore + 1) * 32;
   static constexpr int kQTile = 128 * D * 2;
@@ -226,15 +227,15 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         if (!mbar_wait(rk.at(kv_full), rk.parity ^ 1u)) ok = false;
     }
   } else if (warp >= C::kMma && warp < C::kClean) {
-    // query tiles w0 and w0 + 1; the whole warp walks, one lane issues
-    const int w0 = 2 * (warp - C::kMma);
+    // query tiles w0 .. w0 + kPer - 1; the whole warp walks, one lane issues
+    const int w0 = C::kPer * (warp - C::kMma);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1, 0);
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, kKvHalf, 1024);
     const uint32_t lead = elect_lane();
     Ring<C::kQ> rq;                // of the item's first query tile
     Ring<C::kKv> run, kv, pv_at;   // the run's first tile, this step's K, the pending products' V
-    uint32_t turn[2] = {0, 0};     // parity of p_full
-    bool pend[2] = {false, false};
+    uint32_t turn[C::kPer] = {};   // parity of p_full
+    bool pend[C::kPer] = {};
     int pnt = 0;                   // the pending products' 16-key steps
     bool pfirst = false, plast = false, pfree = false;
     auto products = [&](int u) {   // O_w (+)= P_w V of the previous step
@@ -269,7 +270,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint64_t k = desc_at(kmaj, kvslot(kv.i));
         if (!wait(kv.at(kv_full), kv.parity)) break;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < C::kPer; ++u) {
           if (ok) products(u);
           const int w = w0 + u;
           if (!ok || w >= nact) continue;
@@ -299,7 +300,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       rq.next(nact);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < C::kPer; ++u)
       if (ok) products(u);
     // every MMA of this CTA has completed before tensor memory is freed
     tc_commit_by(lead, smem_u32(&S.done));
@@ -369,6 +370,8 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     Ring<C::kKv> run, rv;  // of V
     rv.next();
     uint32_t s_turn = 0, o_turn = 0;
+    Ring<C::kQ> last;      // the slot of this tile's last item
+    bool staged = false;
     for (; ok && it.next();) {
       const int row = it.r0 + 128 * w + r;
       const size_t grow = (size_t)it.bk * it.R + row;
@@ -505,6 +508,10 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       }
       fence_proxy_async_smem();  // generic writes -> TMA store
       tc_fence_before();
+      // the store warp has taken the last one, else this phase could pass it by
+      if (staged && !wait(last.at(q_empty), last.parity)) break;
+      last = at;
+      staged = true;
       mbar_arrive(o_staged + 8 * w);
       if (valid) {
         if (p.nks > 1) p.part_ml[(size_t)it.split * it.rows + grow] = make_float2(m, l);
