@@ -272,97 +272,179 @@ cudaError_t launch_rope_typed(RopeParams p, cudaStream_t s) {
 }
 
 // ------------------------------------------------ the rotation with the pool
-// One CTA: 256 tokens of one (b, h) of one tensor; thread (t1, slot) turns and
-// sums the 16 rows of level-1 token t1 (16 rows of two chunks), left to right,
-// as the pool kernel does; level 2 from the level-1 means in shared memory.
-// The tensors and heads that share a table row run next to each other.
-constexpr int kPoolRows = 4;  // rows in flight per thread
+// One CTA: 256 tokens of one (b, h) of Q and K, or of V; thread (t1, slot)
+// turns and sums the 16 rows of level-1 token t1 (16 rows of two chunks), left
+// to right, as the pool kernel does; level 2 from the level-1 means in shared
+// memory.  Q and K share the table's row, which is as large as a bf16 head's
+// row of both and comes from the L2 cache for every head but the first.
+// Rows, and the table's, are copied to shared memory kDepth ahead (cp.async;
+// each thread its own chunks, so nothing is synchronised): up to 64 KB a CTA
+// are in flight, without the registers that would cost.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last n groups have landed
+template <int n>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
+
+template <typename T, int D>
+struct PoolShape {
+  static constexpr int kThreads = 16 * D / (2 * Vec16<T>::N);
+  // a thread's part of a row: two chunks of Q and of K, its pairs' turns
+  static constexpr int kTurns = Vec16<T>::N * 8, kPart = 64 + kTurns;
+  static constexpr int kDepth = kThreads <= 64 ? 8 : 512 / kThreads;  // rows ahead
+  static constexpr int kSmem = kDepth * kPart * kThreads + 2 * 16 * D * 4;
+};
 
 template <typename T, int D, bool kInterleaved>
-__global__ void __launch_bounds__(16 * D / (2 * Vec16<T>::N))
+__global__ void __launch_bounds__(PoolShape<T, D>::kThreads)
 rope_pool_kernel(RopeParams p, PoolParams o) {
+  using P = PoolShape<T, D>;
   constexpr int VEC = Vec16<T>::N;
   constexpr int SL = D / (2 * VEC);  // slots per row
-  __shared__ __align__(16) float m1[16][D];
-  const int nt = o.L >= 2 ? 3 : 2;  // V has no level-1 output
+  constexpr int kRow = D / VEC;      // chunks of a row
+  extern __shared__ __align__(16) unsigned char smem[];
+  // ring: [kDepth][chunk of Q, Q, K, K, turns ...][thread] of 16 bytes
+  float* m1 = reinterpret_cast<float*>(smem + P::kDepth * P::kPart * P::kThreads);  // [tensor][16][D]
+  const int kinds = o.L >= 2 ? 2 : 1;  // V has no level-1 output
   long long id = blockIdx.x;
-  const int tensor = (int)(id % nt);
-  id /= nt;
+  const bool is_v = kinds == 2 && (id & 1) != 0;
+  id /= kinds;
   const int bh = (int)(id % o.BH);
   const int chunk = (int)(id / o.BH);
-  const int t1 = threadIdx.x / SL;
+  const int tid = threadIdx.x, t1 = tid / SL;
   const int n1 = o.N / kBlock;
   const int g1 = chunk * 16 + t1;
   const int half = p.rot / 2;
-  const Slot<T> sl(threadIdx.x % SL, half, kInterleaved);
-  const int nrot = tensor < 2 ? sl.nrot : 0;
+  const Slot<T> sl(tid % SL, half, kInterleaved);
+  const int nt = is_v ? 1 : 2;
   if (g1 < n1) {
-    const size_t row0 = (size_t)bh * o.N + (size_t)g1 * kBlock;
-    const uint4* src = static_cast<const uint4*>(p.x[tensor]) + row0 * (D / VEC);
-    uint4* dst = tensor < 2 ? static_cast<uint4*>(p.y[tensor]) + row0 * (D / VEC) : nullptr;
+    const size_t row0 = ((size_t)bh * o.N + (size_t)g1 * kBlock) * kRow;
+    const uint4* src0 = static_cast<const uint4*>(is_v ? p.x[2] : p.x[0]) + row0;
+    const uint4* src1 = static_cast<const uint4*>(p.x[1]) + row0;
+    uint4* dst0 = static_cast<uint4*>(p.y[0]) + row0;
+    uint4* dst1 = static_cast<uint4*>(p.y[1]) + row0;
     const size_t trow = (p.per_batch ? (size_t)(bh / p.H) * o.N : 0) + (size_t)g1 * kBlock;
     const float* tab = p.table + trow * (2 * half);
-    float acc[2 * VEC];
+    constexpr int kLine = P::kThreads * 16;
+    unsigned char* mine = smem + tid * 16;
+    const bool wide = half % 2 == 0 && sl.nrot == VEC;  // turns in pieces of 16 bytes, else of 8
+    auto fetch = [&](int j) {
+      if (j < kBlock) {
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine) + (uint32_t)((j % P::kDepth) * P::kPart * P::kThreads);
+        const float* turns = tab + (size_t)j * (2 * half) + 2 * sl.pair0;
+        if (is_v) {
+        } else if (wide) {
 #pragma unroll
-    for (int j0 = 0; j0 < kBlock; j0 += kPoolRows) {
-      uint4 v[kPoolRows][2];
+          for (int e = 0; e < VEC / 2; ++e) copy16(at + (4 + e) * kLine, turns + 4 * e);
+        } else {
 #pragma unroll
-      for (int j = 0; j < kPoolRows; ++j) {
-        v[j][0] = src[(j0 + j) * (D / VEC) + sl.c0];
-        v[j][1] = src[(j0 + j) * (D / VEC) + sl.c1];
+          for (int e = 0; e < VEC; ++e)
+            if (e < sl.nrot) copy8(at + (4 + e / 2) * kLine + (e & 1) * 8, turns + 2 * e);
+        }
+        copy16(at, src0 + j * kRow + sl.c0);
+        copy16(at + kLine, src0 + j * kRow + sl.c1);
+        if (!is_v) {
+          copy16(at + 2 * kLine, src1 + j * kRow + sl.c0);
+          copy16(at + 3 * kLine, src1 + j * kRow + sl.c1);
+        }
+      }
+      copies_issued();
+    };
+#pragma unroll 1
+    for (int j = 0; j < P::kDepth; ++j) fetch(j);
+    float acc[2][2 * VEC];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 2 * VEC; ++e) acc[t][e] = 0.f;
+#pragma unroll 2
+    for (int j = 0; j < kBlock; ++j) {
+      copies_wait<P::kDepth - 1>();
+      const unsigned char* at = mine + (j % P::kDepth) * P::kPart * P::kThreads;
+      float c[VEC], s[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float4 t = *reinterpret_cast<const float4*>(at + (4 + e) * kLine);
+        const bool on0 = 2 * e < sl.nrot, on1 = 2 * e + 1 < sl.nrot;
+        c[2 * e] = on0 ? t.x : 1.f;
+        s[2 * e] = on0 ? t.y : 0.f;
+        c[2 * e + 1] = on1 ? t.z : 1.f;
+        s[2 * e + 1] = on1 ? t.w : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < kPoolRows; ++j) {
-        if (tensor < 2) {
-          float c[VEC], s[VEC];
-          load_turns<VEC>(tab + (size_t)(j0 + j) * (2 * half), sl.pair0, nrot, 1.f, c, s);
-          turn_slot<T, kInterleaved>(v[j], c, s, nrot);
-          dst[(j0 + j) * (D / VEC) + sl.c0] = v[j][0];
-          dst[(j0 + j) * (D / VEC) + sl.c1] = v[j][1];
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && is_v) break;
+        uint4 v[2] = {*reinterpret_cast<const uint4*>(at + 2 * t * kLine),
+                      *reinterpret_cast<const uint4*>(at + (2 * t + 1) * kLine)};
+        if (!is_v) {
+          turn_slot<T, kInterleaved>(v, c, s, sl.nrot);
+          uint4* dst = (t == 0 ? dst0 : dst1) + j * kRow;
+          dst[sl.c0] = v[0];
+          dst[sl.c1] = v[1];
         }
         float x[2 * VEC];  // the means are of the stored values
-        Vec16<T>::unpack(v[j][0], x);
-        Vec16<T>::unpack(v[j][1], x + VEC);
+        Vec16<T>::unpack(v[0], x);
+        Vec16<T>::unpack(v[1], x + VEC);
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) acc[e] = (j0 + j == 0) ? x[e] : __fadd_rn(acc[e], x[e]);
+        for (int e = 0; e < 2 * VEC; ++e) acc[t][e] = j == 0 ? x[e] : __fadd_rn(acc[t][e], x[e]);
       }
+      fetch(j + P::kDepth);
     }
-    float* o1 = o.lvl[tensor][1];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int d = (w ? sl.c1 : sl.c0) * VEC;
+    for (int t = 0; t < 2; ++t) {
+      if (t == 1 && is_v) break;
+      float* o1 = is_v ? nullptr : (t == 0 ? o.lvl[0][1] : o.lvl[1][1]);
 #pragma unroll
-      for (int e = 0; e < VEC; e += 4) {
-        float4 m;
-        m.x = __fmul_rn(acc[w * VEC + e], 0.0625f);
-        m.y = __fmul_rn(acc[w * VEC + e + 1], 0.0625f);
-        m.z = __fmul_rn(acc[w * VEC + e + 2], 0.0625f);
-        m.w = __fmul_rn(acc[w * VEC + e + 3], 0.0625f);
-        *reinterpret_cast<float4*>(&m1[t1][d + e]) = m;
-        if (o1 != nullptr) *reinterpret_cast<float4*>(o1 + ((size_t)bh * n1 + g1) * D + d + e) = m;
+      for (int w = 0; w < 2; ++w) {
+        const int d = (w ? sl.c1 : sl.c0) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          float4 m;
+          m.x = __fmul_rn(acc[t][w * VEC + e], 0.0625f);
+          m.y = __fmul_rn(acc[t][w * VEC + e + 1], 0.0625f);
+          m.z = __fmul_rn(acc[t][w * VEC + e + 2], 0.0625f);
+          m.w = __fmul_rn(acc[t][w * VEC + e + 3], 0.0625f);
+          *reinterpret_cast<float4*>(m1 + (t * 16 + t1) * D + d + e) = m;
+          if (o1 != nullptr) *reinterpret_cast<float4*>(o1 + ((size_t)bh * n1 + g1) * D + d + e) = m;
+        }
       }
     }
   }
   if (o.L < 2) return;
   __syncthreads();
   // level 2: one level-2 token per CTA (N is a multiple of 256 when L >= 2)
-  for (int d = threadIdx.x; d < D; d += blockDim.x) {
-    float a = m1[0][d];
+  for (int i = tid; i < nt * D; i += P::kThreads) {
+    const int t = i / D, d = i - t * D;
+    const float* m = m1 + t * 16 * D + d;
+    float a = m[0];
 #pragma unroll
-    for (int t = 1; t < 16; ++t) a = __fadd_rn(a, m1[t][d]);
-    o.lvl[tensor][2][((size_t)bh * (o.N >> 8) + chunk) * D + d] = __fmul_rn(a, 0.0625f);
+    for (int k = 1; k < 16; ++k) a = __fadd_rn(a, m[k * D]);
+    float* o2 = is_v ? o.lvl[2][2] : (t == 0 ? o.lvl[0][2] : o.lvl[1][2]);
+    o2[((size_t)bh * (o.N >> 8) + chunk) * D + d] = __fmul_rn(a, 0.0625f);
   }
+}
+
+template <typename T, int D, bool kInterleaved>
+cudaError_t launch_rope_pool_as(const RopeParams& p, const PoolParams& o, cudaStream_t s) {
+  using P = PoolShape<T, D>;
+  const int n1 = o.N / kBlock;
+  const long long blocks = (long long)((n1 + 15) / 16) * o.BH * (o.L >= 2 ? 2 : 1);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<T, D, kInterleaved>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  rope_pool_kernel<T, D, kInterleaved><<<(unsigned)blocks, P::kThreads, P::kSmem, s>>>(p, o);
+  return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_rope_pool_typed(const RopeParams& p, const PoolParams& o, cudaStream_t s) {
-  constexpr int threads = 16 * D / (2 * Vec16<T>::N);
-  const int n1 = o.N / kBlock;
-  const long long blocks = (long long)((n1 + 15) / 16) * o.BH * (o.L >= 2 ? 3 : 2);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (p.interleaved) rope_pool_kernel<T, D, true><<<(unsigned)blocks, threads, 0, s>>>(p, o);
-  else rope_pool_kernel<T, D, false><<<(unsigned)blocks, threads, 0, s>>>(p, o);
-  return cudaGetLastError();
+  return p.interleaved ? launch_rope_pool_as<T, D, true>(p, o, s) : launch_rope_pool_as<T, D, false>(p, o, s);
 }
 
 }  // namespace
