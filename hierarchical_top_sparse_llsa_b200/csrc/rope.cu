@@ -296,7 +296,7 @@ struct PoolShape {
   static constexpr int kThreads = 16 * D / (2 * Vec16<T>::N);
   // a thread's part of a row: two chunks of Q and of K, its pairs' turns
   static constexpr int kTurns = Vec16<T>::N * 8, kPart = 64 + kTurns;
-  static constexpr int kDepth = kThreads <= 64 ? 8 : 512 / kThreads;  // rows ahead
+  static constexpr int kDepth = kThreads <= 64 ? 4 : 512 / kThreads;  // rows ahead
   static constexpr int kSmem = kDepth * kPart * kThreads + 2 * 16 * D * 4;
 };
 
