@@ -386,7 +386,7 @@ int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, const void* 
     const CUtensorMap maps[4] = {qo[0], kv[0], kv[1], qo[1]};
     err = launch_cross_fwd_tc(p, maps, s);
   } else {
-    err = launch_cross_fwd_simt(p, desc->dtype, s);
+    err = launch_cross_fwd_simt(p, s);
   }
   if (err == cudaSuccess && p.nks > 1) err = launch_cross_combine(p, desc->dtype, s);
   return launch_status(err);
@@ -415,7 +415,6 @@ int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* 
   if (!spans_apart(spans, 13, 4)) return LLSA_ERR_INVALID_ARG;
   CrossParams p = cross_params(desc, q, k, v, kv_len, key_mask, dev_status, w.plan);
   p.o_in = o;
-  p.res_in = desc->dtype == LLSA_BF16 ? o_res : nullptr;
   p.lse_in = lse;
   p.dout = dout;
   p.dq = dq;
@@ -444,15 +443,7 @@ int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* 
     if (st != LLSA_OK) return st;
     return launch_status(launch_cross_bwd_tc(p, q128, kv64, kv128, q64, s));
   }
-  cudaError_t e = launch_cross_delta(p, desc->dtype, s);
-  if (e == cudaSuccess) e = launch_cross_bwd_simt(p, desc->dtype, s);
-  if (e == cudaSuccess && p.nks > 1)
-    e = launch_cross_reduce(p.part_dq, dq, p.nks, rows * p.D, p.scale, desc->dtype, s);
-  if (e == cudaSuccess && p.nz > 1) {
-    e = launch_cross_reduce(p.part_dk, dk, p.nz, keys * p.D, p.scale, desc->dtype, s);
-    if (e == cudaSuccess) e = launch_cross_reduce(p.part_dv, dv, p.nz, keys * p.D, 1.f, desc->dtype, s);
-  }
-  return launch_status(e);
+  return launch_status(launch_cross_bwd_simt(p, s));
 }
 
 }  // extern "C"

@@ -26,7 +26,6 @@ struct CrossParams {
   const int32_t* kv_len;   // [B] or null
   const uint8_t* mask;     // [B, S] or null
   const void* o_in;        // bwd: O
-  const void* res_in;      // bwd: bf16 residual of O or null
   const float* lse_in;     // bwd
   const void* dout;
   void* o;
@@ -63,6 +62,25 @@ __device__ __forceinline__ int cross_len(const CrossParams& p, int b) {
   return n < 0 ? 0 : (n > p.S ? p.S : n);
 }
 
+// Whether b sees at most one key (a whole warp asks).
+__device__ __forceinline__ bool sees_one(const CrossParams& p, int b, int len) {
+  if (p.mask == nullptr || len <= 1) return len <= 1;
+  const uint8_t* m = p.mask + (size_t)b * p.S;
+  const int lane = threadIdx.x & 31;
+  int seen = 0;
+  for (int k0 = 0; k0 < len && seen < 2; k0 += 256) {
+    bool on[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + 32 * u + lane;
+      on[u] = k < len && m[k] != 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) seen += __popc(__ballot_sync(0xffffffffu, on[u]));
+  }
+  return seen <= 1;
+}
+
 // How the work is cut, from the sizes alone (workspace sizes follow from it).
 struct CrossPlan {
   int nks, nz;
@@ -80,11 +98,8 @@ cudaError_t launch_cross_fwd_tc(const CrossParams& p, const CUtensorMap* maps, c
 // q128, kv64, kv128, q64: (Q, dO) or (K, V) as above, boxes of 128 or 64 rows; q128[2]: dQ
 cudaError_t launch_cross_bwd_tc(const CrossParams& p, const CUtensorMap* q128, const CUtensorMap* kv64,
                                 const CUtensorMap* kv128, const CUtensorMap* q64, cudaStream_t s);
-cudaError_t launch_cross_fwd_simt(const CrossParams& p, int dtype, cudaStream_t s);
-cudaError_t launch_cross_bwd_simt(const CrossParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cross_fwd_simt(const CrossParams& p, cudaStream_t s);
+cudaError_t launch_cross_bwd_simt(const CrossParams& p, cudaStream_t s);
 cudaError_t launch_cross_combine(const CrossParams& p, int dtype, cudaStream_t s);
-cudaError_t launch_cross_delta(const CrossParams& p, int dtype, cudaStream_t s);
-// out[i] = f * sum over z < n of part[z][i], i < total (a multiple of 8)
-cudaError_t launch_cross_reduce(const float* part, void* out, int n, size_t total, float f, int dtype, cudaStream_t s);
 
 }  // namespace llsa

@@ -1,5 +1,5 @@
 // Cross attention in fp32 on the CUDA cores: forward, dQ, and dK with dV, in
-// tiles of 64 queries x 64 keys.
+// tiles of 64 queries (16 in a short forward) x 64 keys.
 //
 //   s = scale q k^T, P = e^(s - lse), O = P V / l
 //   dV = P^T dO, dS = P (dO V^T - Delta), dQ = scale dS K, dK = scale dS^T Q
@@ -28,22 +28,19 @@ constexpr int kBwdThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-inline int tiles_of(int n) { return n / kT + (n % kT != 0); }
+inline int tiles_of(int n, int t = kT) { return n / t + (n % t != 0); }
 
-// rows r < nrows of src [.., D] (kept where keep is null or keep[r] != 0) as
-// floats into dst rows of LD floats; the others as zeros
-template <typename T, int D, int LD, int THREADS>
-__device__ __forceinline__ void load_rows(float* dst, const T* src, int nrows, const uint8_t* keep) {
-  constexpr int VEC = Vec16<T>::N;
-  for (int e = threadIdx.x; e < kT * (D / VEC); e += THREADS) {
-    const int r = e / (D / VEC), c = (e % (D / VEC)) * VEC;
-    float x[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = 0.f;
-    if (r < nrows && (keep == nullptr || keep[r] != 0)) Vec16<T>::load(src + (size_t)r * D + c, x);
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      *reinterpret_cast<float4*>(dst + r * LD + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+// rows r < nrows of src [.., D] (kept where keep is null or keep[r] != 0) into
+// ROWS dst rows of LD floats; the others as zeros
+template <int D, int LD, int THREADS, int ROWS>
+__device__ __forceinline__ void load_rows(float* dst, const void* src, int nrows, const uint8_t* keep) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += THREADS) {
+    const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nrows && (keep == nullptr || keep[r] != 0))
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + (size_t)r * D + c);
+    *reinterpret_cast<float4*>(dst + r * LD + c) = x;
   }
 }
 
@@ -96,14 +93,16 @@ __device__ __forceinline__ void dot_tile(float (&acc)[R][4], const float* a, con
 constexpr int kLP = kT + 4;  // row length of the probability tiles
 
 // ----------------------------------------------------------------- forward
-template <typename T, int D>
+// R query rows a thread, 8 R a tile
+template <int D, int R>
 __global__ void __launch_bounds__(kFwdThreads)
 cross_fwd_simt(CrossParams p, int qtiles) {
   constexpr int LD = D + 4;
   extern __shared__ __align__(16) float smf[];
   __shared__ uint8_t keep[kT];
-  float* Q = smf;             // [64][LD]
-  float* K = Q + kT * LD;     // [64][LD], then P [64][kLP]
+  constexpr int kQ = 8 * R;
+  float* Q = smf;             // [kQ][LD]
+  float* K = Q + kQ * LD;     // [64][LD], then P [kQ][kLP]
   float* V = K + kT * LD;     // [64][D]
   float* P = K;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -114,18 +113,18 @@ cross_fwd_simt(CrossParams p, int qtiles) {
   const int bh = (int)(id / p.nks);
   const int b = bh / p.H;
   const size_t kvrow = (size_t)bh * p.S;
-  const int q0 = qt * kT, nq = min(kT, p.N - q0);
+  const int q0 = qt * kQ, nq = min(kQ, p.N - q0);
   const size_t row0 = (size_t)bh * p.N + q0;
   const int len = cross_len(p, b);
   const int ktiles = (len + kT - 1) / kT;
   const int kt0 = (int)((long long)ktiles * split / p.nks), kt1 = (int)((long long)ktiles * (split + 1) / p.nks);
   const float sc2 = p.scale * kLog2e;
 
-  load_rows<T, D, LD, kFwdThreads>(Q, static_cast<const T*>(p.q) + row0 * D, nq, nullptr);
-  float o[8][D / 16];
-  float m[8], l[8];
+  load_rows<D, LD, kFwdThreads, kQ>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
+  float o[R][D / 16];
+  float m[R], l[R];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < R; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -137,17 +136,17 @@ cross_fwd_simt(CrossParams p, int qtiles) {
     load_keep(keep, p, b, k0, len);
     __syncthreads();
     const int nk = min(kT, p.S - k0);
-    load_rows<T, D, LD, kFwdThreads>(K, static_cast<const T*>(p.k) + (kvrow + k0) * D, nk, keep);
-    load_rows<T, D, D, kFwdThreads>(V, static_cast<const T*>(p.v) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, LD, kFwdThreads, kT>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, D, kFwdThreads, kT>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
     __syncthreads();
-    float s[8][4];
-    dot_tile<D, 8>(s, Q, K, ty, tx);
+    float s[R][4];
+    dot_tile<D, R>(s, Q, K, ty, tx);
     bool on[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) on[j] = keep[tx + 16 * j] != 0;
     __syncthreads();  // K is read; P takes its place
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -162,7 +161,7 @@ cross_fwd_simt(CrossParams p, int qtiles) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float e = exp2f(s[i][j] - mb);
-        P[(ty * 8 + i) * kLP + tx + 16 * j] = e;
+        P[(ty * R + i) * kLP + tx + 16 * j] = e;
         sum += e;
       }
       l[i] = l[i] * corr + half_sum(sum);
@@ -171,16 +170,16 @@ cross_fwd_simt(CrossParams p, int qtiles) {
     }
     __syncwarp();  // a P row is written and read by one half warp
     for (int j = 0; j < kT; j += 4) {
-      float4 pr[8];
+      float4 pr[R];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pr[i] = *reinterpret_cast<const float4*>(P + (ty * 8 + i) * kLP + j);
+      for (int i = 0; i < R; ++i) pr[i] = *reinterpret_cast<const float4*>(P + (ty * R + i) * kLP + j);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           const float4 v = *reinterpret_cast<const float4*>(V + (j + jj) * D + c * 64 + tx * 4);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < R; ++i) {
             const float w = jj == 0 ? pr[i].x : (jj == 1 ? pr[i].y : (jj == 2 ? pr[i].z : pr[i].w));
             o[i][4 * c] = fmaf(w, v.x, o[i][4 * c]);
             o[i][4 * c + 1] = fmaf(w, v.y, o[i][4 * c + 1]);
@@ -192,8 +191,8 @@ cross_fwd_simt(CrossParams p, int qtiles) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = ty * 8 + i;
+  for (int i = 0; i < R; ++i) {
+    const int r = ty * R + i;
     if (r >= nq) continue;
     const size_t row = row0 + r;
     if (p.nks > 1) {
@@ -206,27 +205,24 @@ cross_fwd_simt(CrossParams p, int qtiles) {
     } else {
       const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;  // 0 without keys; NaN stays NaN
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const size_t at = row * D + (c / 4) * 64 + tx * 4 + (c % 4);
-        const float x = o[i][c] * inv;
-        T y;
-        store_elem(&y, x);
-        static_cast<T*>(p.o)[at] = y;
-        if (sizeof(T) == 2 && p.o_res != nullptr) store_elem(static_cast<bf16*>(p.o_res) + at, x - to_f32(y));
-      }
+      for (int c = 0; c < D / 64; ++c)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * D + c * 64 + tx * 4) =
+            make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
       if (tx == 0) p.lse[row] = l[i] != 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
     }
   }
 }
 
-// The splits of a row joined: one warp per row, in the order of the splits.
-template <typename T, int D>
+// The splits of a row joined, in a fixed order: by a warp, or (kWarps = 8, for
+// eight splits or more) by a block whose warps take every eighth.
+template <typename T, int D, int kWarps>
 __global__ void __launch_bounds__(256)
 cross_combine_kernel(CrossParams p) {
   constexpr int C = D / 32;
+  __shared__ float part[kWarps][D + 1];
   const size_t rows = (size_t)p.B * p.H * p.N;
-  const size_t row = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const size_t row = kWarps == 1 ? (size_t)blockIdx.x * 8 + warp : (size_t)blockIdx.x;
   if (row >= rows) return;
   float m = -INFINITY;
   for (int z = lane; z < p.nks; z += 32) m = fmaxf(m, p.part_ml[z * rows + row].x);
@@ -237,7 +233,7 @@ cross_combine_kernel(CrossParams p) {
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
 #pragma unroll 4
-  for (int z = 0; z < p.nks; ++z) {
+  for (int z = kWarps == 1 ? 0 : warp; z < p.nks; z += kWarps) {
     const float2 ml = p.part_ml[z * rows + row];
     if (ml.x == -INFINITY) continue;  // a split without keys: its O may not be written
     const float w = exp2f(ml.x - mb);
@@ -255,6 +251,19 @@ cross_combine_kernel(CrossParams p) {
       acc[C - 1] = fmaf(v.w, w, acc[C - 1]);
     }
   }
+  if constexpr (kWarps > 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[warp][lane * C + c] = acc[c];
+    if (lane == 0) part[warp][D] = l;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int u = 1; u < kWarps; ++u) {
+      l += part[u][D];
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += part[u][lane * C + c];
+    }
+  }
   const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -269,33 +278,11 @@ cross_combine_kernel(CrossParams p) {
 }
 
 // ---------------------------------------------------------------- backward
-// Delta = dO . (O + residual): a warp per row
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-cross_delta_kernel(CrossParams p) {
-  constexpr int C = D / 32;
-  const size_t rows = (size_t)p.B * p.H * p.N;
-  const size_t row = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  float s = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const size_t at = row * D + lane * C + c;
-    float o = to_f32(static_cast<const T*>(p.o_in)[at]);
-    if (sizeof(T) == 2 && p.res_in != nullptr) o += to_f32(static_cast<const bf16*>(p.res_in)[at]);
-    s = fmaf(o, to_f32(static_cast<const T*>(p.dout)[at]), s);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) p.delta[row] = s;
-}
-
 // The P and dS of a tile, written to shared memory [query][key].
 template <int D>
 __device__ __forceinline__ void p_and_ds(const float* Q, const float* K, const float* dO, const float* V, float* P,
                                          float* dS, const float* lse2, const float* del, const uint8_t* keep,
-                                         float sc2, int ty, int tx) {
+                                         float sc2, bool one, int ty, int tx) {
   float s[4][4], dp[4][4];
   dot_tile<D, 4>(s, Q, K, ty, tx);
   dot_tile<D, 4>(dp, dO, V, ty, tx);
@@ -307,25 +294,38 @@ __device__ __forceinline__ void p_and_ds(const float* Q, const float* K, const f
       const int c = tx + 16 * j;
       const float e = keep[c] != 0 ? exp2f(fmaf(s[i][j], sc2, -lse2[r])) : 0.f;
       P[r * kLP + c] = e;
-      dS[r * kLP + c] = e * (dp[i][j] - del[r]);
+      dS[r * kLP + c] = one ? 0.f : e * (dp[i][j] - del[r]);
     }
   }
 }
 
-// lse2[r], del[r] of 64 query rows; rows past the end take lse = +inf, so
-// that their probabilities are zero
-__device__ __forceinline__ void load_side(float* lse2, float* del, const CrossParams& p, size_t row0, int nq) {
-  if (threadIdx.x < kT) {
-    const bool on = (int)threadIdx.x < nq;
-    lse2[threadIdx.x] = on ? p.lse_in[row0 + threadIdx.x] * kLog2e : INFINITY;
-    del[threadIdx.x] = on ? p.delta[row0 + threadIdx.x] : 0.f;
+// lse2[r] and del[r] = dO . O of 64 query rows, four threads a row; rows past
+// the end take lse = +inf, so that their probabilities are zero.  dO: the tile.
+template <int D>
+__device__ __forceinline__ void load_side(float* lse2, float* del, const float* dO, const CrossParams& p, size_t row0,
+                                          int nq) {
+  const int r = threadIdx.x / 4, q = threadIdx.x % 4;
+  float s = 0.f;
+  if (r < nq) {
+    const float* o = static_cast<const float*>(p.o_in) + (row0 + r) * D;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const float4 x = *reinterpret_cast<const float4*>(o + (4 * c + q) * 4);
+      const float4 y = *reinterpret_cast<const float4*>(dO + r * (D + 4) + (4 * c + q) * 4);
+      s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+    }
+  }
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  if (q == 0) {
+    const float l = r < nq ? p.lse_in[row0 + r] : INFINITY;
+    lse2[r] = l == -INFINITY ? INFINITY : l * kLog2e;  // without keys too
+    del[r] = s;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* dst, const float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) store_elem(dst + i, v[i]);
+__device__ __forceinline__ void store4(float* dst, const float* v) {
+  *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
 template <int D>
@@ -334,17 +334,19 @@ struct BwdSmem {
   static constexpr int kFloats = 4 * kT * LD + 2 * kT * kLP;
 };
 
+struct BwdSide {
+  uint8_t keep[kT];
+  float lse2[kT], del[kT];
+};
+
 // dQ of one query tile over one split of the key tiles.
-template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads)
-cross_dq_simt(CrossParams p, int qtiles) {
+template <int D>
+__device__ __forceinline__ void dq_tile(const CrossParams& p, int qtiles, long long id, float* smf, BwdSide& S) {
   constexpr int LD = D + 4;
-  extern __shared__ __align__(16) float smf[];
-  __shared__ uint8_t keep[kT];
-  __shared__ float lse2[kT], del[kT];
+  uint8_t* keep = S.keep;
+  float *lse2 = S.lse2, *del = S.del;
   float *Q = smf, *dO = Q + kT * LD, *K = dO + kT * LD, *V = K + kT * LD, *P = V + kT * LD, *dS = P + kT * kLP;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  long long id = blockIdx.x;
   const int qt = (int)(id % qtiles);
   id /= qtiles;
   const int split = (int)(id % p.nks);
@@ -356,9 +358,11 @@ cross_dq_simt(CrossParams p, int qtiles) {
   const int len = cross_len(p, b);
   const int ktiles = (len + kT - 1) / kT;
   const int kt0 = (int)((long long)ktiles * split / p.nks), kt1 = (int)((long long)ktiles * (split + 1) / p.nks);
-  load_rows<T, D, LD, kBwdThreads>(Q, static_cast<const T*>(p.q) + row0 * D, nq, nullptr);
-  load_rows<T, D, LD, kBwdThreads>(dO, static_cast<const T*>(p.dout) + row0 * D, nq, nullptr);
-  load_side(lse2, del, p, row0, nq);
+  const bool one = sees_one(p, b, len);
+  load_rows<D, LD, kBwdThreads, kT>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
+  load_rows<D, LD, kBwdThreads, kT>(dO, static_cast<const float*>(p.dout) + row0 * D, nq, nullptr);
+  __syncthreads();
+  load_side<D>(lse2, del, dO, p, row0, nq);
   float acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -369,10 +373,10 @@ cross_dq_simt(CrossParams p, int qtiles) {
     __syncthreads();
     load_keep(keep, p, b, k0, len);
     __syncthreads();
-    load_rows<T, D, LD, kBwdThreads>(K, static_cast<const T*>(p.k) + (kvrow + k0) * D, nk, keep);
-    load_rows<T, D, LD, kBwdThreads>(V, static_cast<const T*>(p.v) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, LD, kBwdThreads, kT>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, LD, kBwdThreads, kT>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
     __syncthreads();
-    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, ty, tx);
+    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, ty, tx);
     __syncwarp();  // a dS row is written and read by one half warp
     for (int j = 0; j < kT; ++j) {
       float w[4];
@@ -404,23 +408,21 @@ cross_dq_simt(CrossParams p, int qtiles) {
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = acc[i][4 * c + e] * p.scale;
-        store4(static_cast<T*>(p.dq) + at, x);
+        store4(static_cast<float*>(p.dq) + at, x);
       }
     }
   }
 }
 
 // dK and dV of one key tile over one segment of the query tiles.
-template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads)
-cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
+template <int D>
+__device__ __forceinline__ void dkv_tile(const CrossParams& p, int qtiles, int ktiles, long long id, float* smf,
+                                         BwdSide& S) {
   constexpr int LD = D + 4;
-  extern __shared__ __align__(16) float smf[];
-  __shared__ uint8_t keep[kT];
-  __shared__ float lse2[kT], del[kT];
+  uint8_t* keep = S.keep;
+  float *lse2 = S.lse2, *del = S.del;
   float *Q = smf, *dO = Q + kT * LD, *K = dO + kT * LD, *V = K + kT * LD, *P = V + kT * LD, *dS = P + kT * kLP;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  long long id = blockIdx.x;
   const int kt = (int)(id % ktiles);
   id /= ktiles;
   const int z = (int)(id % p.nz);
@@ -429,10 +431,11 @@ cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
   const int k0 = kt * kT, nk = min(kT, p.S - k0);
   const size_t kvrow = (size_t)bh * p.S + k0;
   const int len = cross_len(p, b);
+  const bool one = sees_one(p, b, len);
   load_keep(keep, p, b, k0, len);
   __syncthreads();
-  load_rows<T, D, LD, kBwdThreads>(K, static_cast<const T*>(p.k) + kvrow * D, nk, keep);
-  load_rows<T, D, LD, kBwdThreads>(V, static_cast<const T*>(p.v) + kvrow * D, nk, keep);
+  load_rows<D, LD, kBwdThreads, kT>(K, static_cast<const float*>(p.k) + kvrow * D, nk, keep);
+  load_rows<D, LD, kBwdThreads, kT>(V, static_cast<const float*>(p.v) + kvrow * D, nk, keep);
   float ak[4][D / 16], av[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -444,11 +447,12 @@ cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
     const int q0 = qt * kT, nq = min(kT, p.N - q0);
     const size_t row0 = (size_t)bh * p.N + q0;
     __syncthreads();
-    load_rows<T, D, LD, kBwdThreads>(Q, static_cast<const T*>(p.q) + row0 * D, nq, nullptr);
-    load_rows<T, D, LD, kBwdThreads>(dO, static_cast<const T*>(p.dout) + row0 * D, nq, nullptr);
-    load_side(lse2, del, p, row0, nq);
+    load_rows<D, LD, kBwdThreads, kT>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
+    load_rows<D, LD, kBwdThreads, kT>(dO, static_cast<const float*>(p.dout) + row0 * D, nq, nullptr);
     __syncthreads();
-    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, ty, tx);
+    load_side<D>(lse2, del, dO, p, row0, nq);
+    __syncthreads();
+    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, ty, tx);
     __syncthreads();
     for (int r = 0; r < kT; ++r) {
       const float4 w = *reinterpret_cast<const float4*>(P + r * kLP + ty * 4);
@@ -487,16 +491,34 @@ cross_dkv_simt(CrossParams p, int qtiles, int ktiles) {
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = ak[i][4 * c + e] * p.scale;
-        store4(static_cast<T*>(p.dk) + at, x);
-        store4(static_cast<T*>(p.dv) + at, &av[i][4 * c]);
+        store4(static_cast<float*>(p.dk) + at, x);
+        store4(static_cast<float*>(p.dv) + at, &av[i][4 * c]);
       }
     }
   }
 }
 
-template <typename T>
+// The blocks of dK and dV, which are the longer ones, then those of dQ: one
+// launch, for neither alone fills the GPU in a short problem.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads)
+cross_bwd_simt(CrossParams p, int qtiles, int ktiles, int dkv_blocks) {
+  extern __shared__ __align__(16) float smf[];
+  __shared__ BwdSide S;
+  const long long id = blockIdx.x;
+  if (id < dkv_blocks) dkv_tile<D>(p, qtiles, ktiles, id, smf, S);
+  else dq_tile<D>(p, qtiles, id - dkv_blocks, smf, S);
+}
+
+// The parts of dQ, dK and dV (blockIdx.y, from `first`) summed in order.
 __global__ void __launch_bounds__(256)
-cross_reduce_kernel(const float* __restrict__ part, T* __restrict__ out, int n, size_t total, float f) {
+cross_reduce_kernel(CrossParams p, int first) {
+  const int which = first + blockIdx.y;
+  const size_t total = (size_t)p.B * p.H * (which == 0 ? p.N : p.S) * p.D;
+  const float* part = which == 0 ? p.part_dq : (which == 1 ? p.part_dk : p.part_dv);
+  float* out = static_cast<float*>(which == 0 ? p.dq : (which == 1 ? p.dk : p.dv));
+  const int n = which == 0 ? p.nks : p.nz;
+  const float f = which == 2 ? 1.f : p.scale;
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= total) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -508,8 +530,7 @@ cross_reduce_kernel(const float* __restrict__ part, T* __restrict__ out, int n, 
     a.z += v.z;
     a.w += v.w;
   }
-  const float x[4] = {a.x * f, a.y * f, a.z * f, a.w * f};
-  store4(out + i, x);
+  *reinterpret_cast<float4*>(out + i) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
 }
 
 template <typename K>
@@ -517,92 +538,82 @@ cudaError_t allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int D>
+// Query rows a thread of the forward: tiles of 16 rows where 64 would be mostly
+// empty, or would leave SMs without a block however the keys are cut.
+inline int fwd_rows(long long BH, int N, int S) {
+  return N <= 32 || BH * tiles_of(N) * ((tiles_of(S) + 1) / 2) < kCrossSms ? 2 : 8;
+}
+
+template <int D, int R>
 cudaError_t fwd_typed(const CrossParams& p, cudaStream_t s) {
-  const int qt = tiles_of(p.N);
+  const int qt = tiles_of(p.N, 8 * R);
   const long long blocks = (long long)p.B * p.H * p.nks * qt;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)(2 * kT * (D + 4) + kT * D) * sizeof(float);
-  cudaError_t e = allow_smem(cross_fwd_simt<T, D>, smem);
+  const size_t smem = (size_t)((8 * R + kT) * (D + 4) + kT * D) * sizeof(float);
+  cudaError_t e = allow_smem(cross_fwd_simt<D, R>, smem);
   if (e != cudaSuccess) return e;
-  cross_fwd_simt<T, D><<<(unsigned)blocks, kFwdThreads, smem, s>>>(p, qt);
+  cross_fwd_simt<D, R><<<(unsigned)blocks, kFwdThreads, smem, s>>>(p, qt);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t bwd_typed(const CrossParams& p, cudaStream_t s) {
   const int qt = tiles_of(p.N), kt = tiles_of(p.S);
   const long long b1 = (long long)p.B * p.H * p.nks * qt, b2 = (long long)p.B * p.H * p.nz * kt;
-  if (b1 > 0x7fffffffLL || b2 > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (b1 + b2 > 0x7fffffffLL) return cudaErrorInvalidValue;
   const size_t smem = BwdSmem<D>::kFloats * sizeof(float);
-  cudaError_t e = allow_smem(cross_dq_simt<T, D>, smem);
-  if (e == cudaSuccess) e = allow_smem(cross_dkv_simt<T, D>, smem);
+  cudaError_t e = allow_smem(cross_bwd_simt<D>, smem);
   if (e != cudaSuccess) return e;
-  cross_dq_simt<T, D><<<(unsigned)b1, kBwdThreads, smem, s>>>(p, qt);
+  cross_bwd_simt<D><<<(unsigned)(b1 + b2), kBwdThreads, smem, s>>>(p, qt, kt, (int)b2);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.S == 0) return e;
-  cross_dkv_simt<T, D><<<(unsigned)b2, kBwdThreads, smem, s>>>(p, qt, kt);
+  const int first = p.nks > 1 ? 0 : 1, last = p.nz > 1 ? 2 : 0;
+  if (e != cudaSuccess || first > last) return e;
+  const size_t rows = first == 0 && last == 2 ? (size_t)max(p.N, p.S) : (size_t)(first == 0 ? p.N : p.S);
+  const size_t blocks = (p.B * (size_t)p.H * rows * p.D / 4 + 255) / 256;
+  if (blocks > 0x7fffffffULL) return cudaErrorInvalidValue;
+  cross_reduce_kernel<<<dim3((unsigned)blocks, last - first + 1), 256, 0, s>>>(p, first);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t rows_typed(const CrossParams& p, bool combine, cudaStream_t s) {
-  const size_t blocks = ((size_t)p.B * p.H * p.N + 7) / 8;
-  if (blocks > 0x7fffffffULL) return cudaErrorInvalidValue;
-  if (combine) cross_combine_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(p);
-  else cross_delta_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(p);
+cudaError_t combine_typed(const CrossParams& p, cudaStream_t s) {
+  const size_t rows = (size_t)p.B * p.H * p.N;
+  if (p.nks >= 8) cross_combine_kernel<T, D, 8><<<(unsigned)rows, 256, 0, s>>>(p);
+  else cross_combine_kernel<T, D, 1><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t rows_dispatch(const CrossParams& p, int dtype, bool combine, cudaStream_t s) {
-  if (dtype == LLSA_BF16) return p.D == 64 ? rows_typed<bf16, 64>(p, combine, s) : rows_typed<bf16, 128>(p, combine, s);
-  return p.D == 64 ? rows_typed<float, 64>(p, combine, s) : rows_typed<float, 128>(p, combine, s);
-}
-
-// parts of n tiles so that units * parts reaches about two blocks per SM
+// parts of n tiles, two tiles or more in each, so that units * parts reaches
+// about two blocks per SM
 int parts_for(long long units, int n) {
-  if (n < 1) return 1;
-  long long parts = (2LL * kCrossSms + units - 1) / units;
-  if (parts > n) parts = n;
+  long long parts = 2LL * kCrossSms / units;
+  if (parts > (n + 1) / 2) parts = (n + 1) / 2;
   return parts < 1 ? 1 : (int)parts;
 }
 
 }  // namespace
 
-CrossPlan cross_simt_fwd_plan(long long BH, int N, int S) { return {parts_for(BH * tiles_of(N), tiles_of(S)), 1}; }
+CrossPlan cross_simt_fwd_plan(long long BH, int N, int S) {
+  return {parts_for(BH * tiles_of(N, 8 * fwd_rows(BH, N, S)), tiles_of(S)), 1};
+}
 
 CrossPlan cross_simt_bwd_plan(long long BH, int N, int S) {
   return {parts_for(BH * tiles_of(N), tiles_of(S)), parts_for(BH * (S > 0 ? tiles_of(S) : 1), tiles_of(N))};
 }
 
-cudaError_t launch_cross_fwd_simt(const CrossParams& p, int dtype, cudaStream_t s) {
-  if (dtype == LLSA_BF16) return p.D == 64 ? fwd_typed<bf16, 64>(p, s) : fwd_typed<bf16, 128>(p, s);
-  return p.D == 64 ? fwd_typed<float, 64>(p, s) : fwd_typed<float, 128>(p, s);
+cudaError_t launch_cross_fwd_simt(const CrossParams& p, cudaStream_t s) {
+  const bool few = fwd_rows((long long)p.B * p.H, p.N, p.S) == 2;
+  if (p.D == 64) return few ? fwd_typed<64, 2>(p, s) : fwd_typed<64, 8>(p, s);
+  return few ? fwd_typed<128, 2>(p, s) : fwd_typed<128, 8>(p, s);
 }
 
-cudaError_t launch_cross_bwd_simt(const CrossParams& p, int dtype, cudaStream_t s) {
-  if (dtype == LLSA_BF16) return p.D == 64 ? bwd_typed<bf16, 64>(p, s) : bwd_typed<bf16, 128>(p, s);
-  return p.D == 64 ? bwd_typed<float, 64>(p, s) : bwd_typed<float, 128>(p, s);
+cudaError_t launch_cross_bwd_simt(const CrossParams& p, cudaStream_t s) {
+  return p.D == 64 ? bwd_typed<64>(p, s) : bwd_typed<128>(p, s);
 }
 
 cudaError_t launch_cross_combine(const CrossParams& p, int dtype, cudaStream_t s) {
-  return rows_dispatch(p, dtype, true, s);
-}
-
-cudaError_t launch_cross_delta(const CrossParams& p, int dtype, cudaStream_t s) {
-  return rows_dispatch(p, dtype, false, s);
-}
-
-cudaError_t launch_cross_reduce(const float* part, void* out, int n, size_t total, float f, int dtype,
-                                cudaStream_t s) {
-  if (total == 0) return cudaSuccess;
-  const size_t blocks = (total / 4 + 255) / 256;
-  if (blocks > 0x7fffffffULL) return cudaErrorInvalidValue;
-  if (dtype == LLSA_BF16)
-    cross_reduce_kernel<bf16><<<(unsigned)blocks, 256, 0, s>>>(part, static_cast<bf16*>(out), n, total, f);
-  else
-    cross_reduce_kernel<float><<<(unsigned)blocks, 256, 0, s>>>(part, static_cast<float*>(out), n, total, f);
-  return cudaGetLastError();
+  if (dtype == LLSA_BF16) return p.D == 64 ? combine_typed<bf16, 64>(p, s) : combine_typed<bf16, 128>(p, s);
+  return p.D == 64 ? combine_typed<float, 64>(p, s) : combine_typed<float, 128>(p, s);
 }
 
 }  // namespace llsa

@@ -203,25 +203,6 @@ __device__ __forceinline__ uint2 three_terms(float x) {
   return make_uint2(pack_bf16(h, m), pack_bf16(m0 - m, 0.f));
 }
 
-// Whether b sees at most one key (a whole warp asks).
-__device__ __forceinline__ bool sees_one(const CrossParams& p, int b, int len) {
-  if (p.mask == nullptr || len <= 1) return len <= 1;
-  const uint8_t* m = p.mask + (size_t)b * p.S;
-  const int lane = threadIdx.x & 31;
-  int seen = 0;
-  for (int k0 = 0; k0 < len && seen < 2; k0 += 256) {
-    bool on[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int k = k0 + 32 * u + lane;
-      on[u] = k < len && m[k] != 0;
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) seen += __popc(__ballot_sync(0xffffffffu, on[u]));
-  }
-  return seen <= 1;
-}
-
 template <int D, bool kDq>
 __global__ void __launch_bounds__(Cfg<D, kDq>::kThreads, 1)
 cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap ta2,
