@@ -52,6 +52,7 @@ struct CrossParams {
   int nks;         // splits of the keys (fwd: of O; bwd: of dQ)
   int nz;          // bwd: segments of the query tiles (dK, dV)
   CrossRuns runs;  // bf16: what each CTA does
+  int items;       // bwd of bf16: of the first pass
   float scale;
 };
 

@@ -56,11 +56,15 @@ struct Sizes {
   static constexpr int kStages = (D == 64) ? 3 : 2;
   static constexpr int kEpi = kStages * 4;  // first epilogue warp
   static constexpr int kLoad = kEpi + 4, kMma = kLoad + 1, kProd = kMma + 1, kAux = kProd + 1;
-  static constexpr int kAuxWarps = (D == 64) ? 4 : 2;  // each has every kAuxWarps-th tile
+  // Each aux warp has every kAuxWarps-th tile.  kAuxWarps divides kSlots, so a
+  // warp sees every round of its slots: a barrier is not waited for before the
+  // round before has been seen, which its parity would not tell apart.
+  static constexpr int kAuxWarps = 3;
   static constexpr int kThreads = (kAux + kAuxWarps) * 32;
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
   static constexpr int kSlots = (D == 64) ? 6 : 3;
+  static_assert(kSlots % kAuxWarps == 0, "a slot belongs to one aux warp");
   static constexpr uint32_t kColAcc = 128 * kStages;  // S | dP of each stage, accA | accB
 };
 
@@ -106,7 +110,8 @@ struct Cfg : Sizes<D> {
 };
 
 // The items of a CTA, in order.  First pass: 128 query rows against one range
-// of the keys.  Second pass: 128 keys (a key tile) against one range of the
+// of the keys, every grid-th item, so that batch entries of unlike lengths are
+// shared out.  Second pass: 128 keys (a key tile) against one range of the
 // queries.  There the CTA's run is of pairs of a key tile and a tile of 64
 // queries, the queries innermost, or of key tiles (nz == 1).
 template <bool kDq>
@@ -114,31 +119,34 @@ struct BwdItems {
   const CrossParams& p;
   int i, end, nt, nq;          // kDq: items; else key tiles; nt: row tiles per head; nq: query tiles of a head
   int64_t beg, fin;            // second pass: the CTA's pairs
-  int bk, b, split, tile, r0, len;
+  int step_runs, step_tiles;   // first pass: grid in row tiles
+  int run, bk, b, split, tile, r0, len;
   int n0, n;                   // first tile of 64 streamed rows, how many
+  bool started;
 
-  __device__ __forceinline__ BwdItems(const CrossParams& p_) : p(p_), b(-1) {
-    beg = p.runs.begin(blockIdx.x);
-    fin = p.runs.begin(blockIdx.x + 1);
+  __device__ __forceinline__ BwdItems(const CrossParams& p_) : p(p_), b(-1), started(false) {
     nq = (p.N + 63) / 64;
     nt = ((kDq ? p.N : p.S) + 127) / 128;
-    if (!kDq && p.nz > 1) {
-      i = (int)(beg / nq) - 1;
-      end = (int)((fin + nq - 1) / nq);
+    if (kDq) {
+      i = blockIdx.x;
+      end = p.items;
+      step_runs = gridDim.x / nt;
+      step_tiles = gridDim.x - step_runs * nt;
     } else {
-      i = (int)beg - 1;
-      end = (int)fin;
+      beg = p.runs.begin(blockIdx.x);
+      fin = p.runs.begin(blockIdx.x + 1);
+      i = (int)(p.nz > 1 ? beg / nq : beg);
+      end = (int)(p.nz > 1 ? (fin + nq - 1) / nq : fin);
     }
-    const int run = (i + 1) / nt;
-    tile = i - run * nt;  // of the item before the first
-    bk = kDq ? run / p.nks : run;
-    split = kDq ? run - bk * p.nks : 0;
-    range();
+    run = i / nt;
+    tile = i - run * nt;
+    if (i < end) range();
   }
   // what the head and the range of the keys settle
   __device__ __forceinline__ void range() {
+    bk = kDq && p.nks > 1 ? run / p.nks : run;
+    split = run - bk * (kDq ? p.nks : 1);
     const int nb = bk / p.H;
-    if (nb >= p.B) return;  // past the last item
     if (nb != b) {
       b = nb;
       len = cross_len(p, b);
@@ -154,15 +162,19 @@ struct BwdItems {
     }
   }
   __device__ __forceinline__ bool next() {
-    if (++i >= end) return false;
-    if (++tile == nt) {
-      tile = 0;
-      if (!kDq || ++split == p.nks) {
-        split = 0;
-        ++bk;
+    if (started) {
+      const int last = run;
+      i += kDq ? gridDim.x : 1;
+      run += kDq ? step_runs : 0;
+      tile += kDq ? step_tiles : 1;
+      if (tile >= nt) {
+        tile -= nt;
+        ++run;
       }
-      range();
+      if (i < end && run != last) range();
     }
+    started = true;
+    if (i >= end) return false;
     r0 = tile * 128;
     if (!kDq) {
       n0 = 0;
@@ -177,12 +189,21 @@ struct BwdItems {
     }
     return true;
   }
-  // the query row that row r of the next item is (its head's first where there is none)
+  // first pass: the query row that row r of the item after this one is (of the
+  // first item, before the first next()); any row where there is none
   __device__ __forceinline__ size_t peek(int r) const {
-    const bool same = tile + 1 < nt;
-    const int nbk = same || split + 1 < p.nks ? bk : bk + 1;
-    const int row = same ? (tile + 1) * 128 + r : r;
-    return (size_t)(i + 1 < end ? nbk : bk) * p.N + (row < p.N ? row : 0);
+    int ti = tile, ru = run;
+    if (started) {
+      ti += step_tiles;
+      ru += step_runs;
+      if (ti >= nt) {
+        ti -= nt;
+        ++ru;
+      }
+      if (i + (int)gridDim.x >= end) return 0;
+    }
+    const int row = ti * 128 + r;
+    return (size_t)(p.nks > 1 ? ru / p.nks : ru) * p.N + (row < p.N ? row : 0);
   }
   // 16-row steps of the item's tile j
   __device__ __forceinline__ int steps(int j) const {
@@ -644,15 +665,17 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         bool have_c = false;
         uint64_t c2 = 0, ls = 0, ds = 0;
         for (; j < it.n; j += NG, rn.next(NG), turn ^= 1u) {
-          const bool s_seen = look(s_full + 8 * g, turn);
-          if (clean && !wait(rn.at(n_aux), rn.parity)) break;
-          if (!have_c && j > 0) {  // another group has the item's first tile
-            if (!wait(rx.at(c_full), rx.parity)) break;
+          // S first: it tells that the rounds before of the other two are over,
+          // which this group may not have seen
+          if (!wait(s_full + 8 * g, turn)) break;
+          const bool other = !have_c && j > 0;  // another group has the item's first tile
+          const bool x_seen = !clean || look(rn.at(n_aux), rn.parity), c_seen = !other || look(rx.at(c_full), rx.parity);
+          if (!finish(x_seen, rn.at(n_aux), rn.parity) || !finish(c_seen, rx.at(c_full), rx.parity)) break;
+          if (other) {
             const float c0 = S.side.c[rx.i][r];
             c2 = f2_make(c0, c0);
             have_c = true;
           }
-          if (!finish(s_seen, s_full + 8 * g, turn)) break;
           tc_fence_after();
           const int nt = it.steps(j), left = it.len - (it.n0 + j) * 64;
           if (clean || left < 64) {
@@ -842,8 +865,8 @@ cudaError_t launch_typed(CrossParams p, const CUtensorMap* q128, const CUtensorM
                          const CUtensorMap* q64, cudaStream_t s) {
   const int64_t items = (int64_t)p.B * p.H * p.nks * cross_tiles(p.N, 128);
   int grid = (int)(items < kCrossSms ? items : kCrossSms);
-  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  p.runs = cross_runs(items, grid);
+  if (items > 0x7fffff00LL) return cudaErrorInvalidValue;  // and the grid on top
+  p.items = (int)items;
   cudaError_t e = launch_pass<D, true>(p, q128, kv64, q128[2], grid, s);
   const size_t rows = (size_t)p.B * p.H * p.N;
   if (e == cudaSuccess && p.nks > 1) {

@@ -484,9 +484,9 @@ LLSA_API size_t llsa_cross_bwd_workspace_bytes(const llsa_cross_desc* desc);
  *   (values outside [0, S] count as the nearer end); NULL: all S.
  *   key_mask: uint8 [B, S] or NULL.  A state with a zero is not seen.  What k
  *   and v hold at states that are not seen is of no effect, NaN included.
- *   o_res: [B, H, N, D] bf16 or NULL; the bf16 rounding residual of O, as
- *   llsa_attn_fwd_res writes it, for a more exact backward (dtype LLSA_F32:
- *   not used).
+ *   o_res: [B, H, N, D] bf16 or NULL; written with the bf16 rounding residual
+ *   of O, as llsa_attn_fwd_res does, for callers that need O more exactly
+ *   (dtype LLSA_F32: not used).
  *   lse: fp32 [B, H, N], written.
  *   ws: device scratch of ws_bytes >= llsa_cross_fwd_workspace_bytes(desc),
  *   256-byte aligned (may be NULL when that is 0); not read before it is
@@ -501,19 +501,22 @@ LLSA_API int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, con
 
 /*
  * llsa_cross_attn_bwd - gradients of llsa_cross_attn_fwd.
- *   With P_ij = e^{s_ij - lse_i} and Delta_i = dO_i . O_i:
+ *   With P_ij = e^{s_ij - lse_i} and Delta_i = sum_j P_ij (dO_i . v_j):
  *     dS_ij = P_ij (dO_i . v_j - Delta_i)
  *     dQ_i  = sm_scale * sum_j dS_ij k_j
  *     dk_j  = sm_scale * sum_i dS_ij q_i ,  dv_j = sum_i P_ij dO_i
  *   with the sums over i running over every query head that reads the key
- *   head.  States that are not seen get zero gradients.
- *   o, lse: the forward's outputs.  o_res: the forward's residual or NULL;
- *   with it Delta_i = dO_i . (o_i + o_res_i).  dout: dO.  dq: [B, H, N, D],
- *   dk, dv: [B, Hkv, S, D], of dtype, written (dk, dv may be NULL when S = 0).
- *   All 16-byte aligned.  kv_len, key_mask: as the forward took them.
+ *   head.  States that are not seen get zero gradients, and so do the scores of
+ *   a query that sees one state only (its probability is 1 whatever the score).
+ *   o, lse: the forward's outputs.  dtype LLSA_F32 takes Delta_i = dO_i . o_i;
+ *   with LLSA_BF16 o must be valid but is not read, nor is o_res (may be NULL):
+ *   Delta is formed from unrounded terms, as O itself is stored rounded.
+ *   dout: dO.  dq: [B, H, N, D], dk, dv: [B, Hkv, S, D], of dtype, written (dk,
+ *   dv may be NULL when S = 0).  All 16-byte aligned.  kv_len, key_mask: as the
+ *   forward took them.
  *   ws: device scratch of ws_bytes >= llsa_cross_bwd_workspace_bytes(desc),
  *   256-byte aligned (may be NULL when that is 0); not read before it is
- *   written.  dev_status: may be NULL.
+ *   written.  dev_status: may be NULL; LLSA_DEV_TIMEOUT as above.
  *   Outputs and ws overlap nothing (else LLSA_ERR_INVALID_ARG).  Sums run in a
  *   fixed order without global atomics: results are identical from run to run.
  */
