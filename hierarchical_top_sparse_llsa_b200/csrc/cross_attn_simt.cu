@@ -63,24 +63,20 @@ __device__ __forceinline__ float half_sum(float x) {
   return x;
 }
 
-// acc[i][j] = a row (ty * R + i) . b row (tx + 16 j)
-template <int D, int R>
-__device__ __forceinline__ void dot_tile(float (&acc)[R][4], const float* a, const float* b, int ty, int tx) {
+// of the columns j < J
+template <int D, int R, int J>
+__device__ __forceinline__ void dot_part(float (&acc)[R][4], const float* a, const float* b, int ty, int tx) {
   constexpr int LD = D + 4;
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 2
   for (int d = 0; d < D; d += 4) {
-    float4 y[4];
+    float4 y[J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * LD + d);
+    for (int j = 0; j < J; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * LD + d);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float4 x = *reinterpret_cast<const float4*>(a + (ty * R + i) * LD + d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         acc[i][j] = fmaf(x.x, y[j].x, acc[i][j]);
         acc[i][j] = fmaf(x.y, y[j].y, acc[i][j]);
         acc[i][j] = fmaf(x.z, y[j].z, acc[i][j]);
@@ -88,6 +84,19 @@ __device__ __forceinline__ void dot_tile(float (&acc)[R][4], const float* a, con
       }
     }
   }
+}
+
+// acc[i][j] = a row (ty * R + i) . b row (tx + 16 j), of the first n rows of b
+// (16 more at a time)
+template <int D, int R>
+__device__ __forceinline__ void dot_tile(float (&acc)[R][4], const float* a, const float* b, int n, int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  if (n > 32) dot_part<D, R, 4>(acc, a, b, ty, tx);
+  else if (n > 16) dot_part<D, R, 2>(acc, a, b, ty, tx);
+  else dot_part<D, R, 1>(acc, a, b, ty, tx);
 }
 
 constexpr int kLP = kT + 4;  // row length of the probability tiles
@@ -140,7 +149,7 @@ cross_fwd_simt(CrossParams p, int qtiles) {
     load_rows<D, D, kFwdThreads, kT>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
     __syncthreads();
     float s[R][4];
-    dot_tile<D, R>(s, Q, K, ty, tx);
+    dot_tile<D, R>(s, Q, K, nk, ty, tx);
     bool on[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) on[j] = keep[tx + 16 * j] != 0;
@@ -169,7 +178,7 @@ cross_fwd_simt(CrossParams p, int qtiles) {
       for (int c = 0; c < D / 16; ++c) o[i][c] *= corr;
     }
     __syncwarp();  // a P row is written and read by one half warp
-    for (int j = 0; j < kT; j += 4) {
+    for (int j = 0; j < nk; j += 4) {
       float4 pr[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) pr[i] = *reinterpret_cast<const float4*>(P + (ty * R + i) * kLP + j);
@@ -282,10 +291,10 @@ cross_combine_kernel(CrossParams p) {
 template <int D>
 __device__ __forceinline__ void p_and_ds(const float* Q, const float* K, const float* dO, const float* V, float* P,
                                          float* dS, const float* lse2, const float* del, const uint8_t* keep,
-                                         float sc2, bool one, int ty, int tx) {
+                                         float sc2, bool one, int nk, int ty, int tx) {
   float s[4][4], dp[4][4];
-  dot_tile<D, 4>(s, Q, K, ty, tx);
-  dot_tile<D, 4>(dp, dO, V, ty, tx);
+  dot_tile<D, 4>(s, Q, K, nk, ty, tx);
+  dot_tile<D, 4>(dp, dO, V, nk, ty, tx);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i;
@@ -376,9 +385,9 @@ __device__ __forceinline__ void dq_tile(const CrossParams& p, int qtiles, long l
     load_rows<D, LD, kBwdThreads, kT>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep);
     load_rows<D, LD, kBwdThreads, kT>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
     __syncthreads();
-    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, ty, tx);
+    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, nk, ty, tx);
     __syncwarp();  // a dS row is written and read by one half warp
-    for (int j = 0; j < kT; ++j) {
+    for (int j = 0; j < nk; ++j) {
       float w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = dS[(ty * 4 + i) * kLP + j];
@@ -452,7 +461,7 @@ __device__ __forceinline__ void dkv_tile(const CrossParams& p, int qtiles, int k
     __syncthreads();
     load_side<D>(lse2, del, dO, p, row0, nq);
     __syncthreads();
-    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, ty, tx);
+    p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, nk, ty, tx);
     __syncthreads();
     for (int r = 0; r < kT; ++r) {
       const float4 w = *reinterpret_cast<const float4*>(P + r * kLP + ty * 4);

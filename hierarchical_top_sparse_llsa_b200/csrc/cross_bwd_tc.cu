@@ -16,9 +16,10 @@
 // number c per row, dS = P (dP - c) + P (c - Delta), so
 //   dQ = scale (sum_j P (dP - c) K + (c - Delta) sum_j P K),
 //   Delta = c sum_j P + sum_j P (dP - c);
-// c, the mean of dP over the first keys, takes off what the values have in
-// common, so the rounding of P (dP - c) to bf16 is that of dS, and all of it is
-// exact in c.  (Delta from the stored O would carry O's rounding to bf16, which
+// c is what the item's first 16 keys tell of Delta: their part of the sum, and
+// their mean for the probability that the other keys have.  It takes off what
+// the values have in common, so the rounding of P (dP - c) to bf16 is about
+// that of dS, and all of it is exact in c.  (Delta from the stored O would carry O's rounding to bf16, which
 // the keys' common part lifts above the gradient where many keys share a row.)
 // A query that sees one key alone has dS = 0: P is 1 whatever the score.
 //
@@ -689,16 +690,22 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
             }
           }
           if (!have_c) {
-            float d[16];
+            float x[16], d[16];
+            tmem_ld16(ts, x);
             tmem_ld16(ts + 64, d);
             tmem_wait_ld();
-            float t = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) t += d[i];
             uint32_t bits = 0xffffu;
             if (clean) bits = S.bits[rn.i][0] & 0xffffu;
             else if (left < 16) bits = (1u << left) - 1u;
-            const float c0 = t / (float)max(1, __popc(bits));
+            float w = 0.f, wd = 0.f, t = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e = ex2_approx(fmaf(x[i], sc2, nl));
+              w += e;
+              wd = fmaf(e, d[i], wd);
+              t += d[i];
+            }
+            const float c0 = fmaf(1.f - w, t / (float)max(1, __popc(bits)), wd);
             c2 = f2_make(c0, c0);
             have_c = true;
             if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;

@@ -488,7 +488,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = l != 0.f ? o[i] * inv : 0.f;
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
           uint4* rdst = p.o_res != nullptr && valid
                             ? reinterpret_cast<uint4*>(static_cast<bf16*>(p.o_res) + grow * D + c) : nullptr;
 #pragma unroll

@@ -36,43 +36,67 @@ __device__ __forceinline__ uint32_t even_bits(uint32_t v) {
   return v;
 }
 
-// Thread (r, j): pairs 2 j and 2 j + 1 of rows r, r + step, ...  The angle is
-// held in turns: position * (f / 2 pi) in fp64, its whole turns taken off
-// exactly (x - rint(x) is exact), and only the remainder in [-1/2, 1/2] is
+// Cosine and sine, times m, of position x at `turns` turns a position.  The
+// angle is held in turns: position * (f / 2 pi) in fp64, its whole turns taken
+// off exactly (x - rint(x) is exact), and only the remainder in [-1/2, 1/2] is
 // rounded to fp32 (sincospi of twice it), so the angle's error is 2^-53 of the
 // turns made plus 2^-24 of a half turn at any position.
+__device__ __forceinline__ float2 turn_of(int x, double turns, float m) {
+  const double t = (double)x * turns;
+  float s, c;
+  sincospif(2.0f * (float)(t - rint(t)), &s, &c);
+  return make_float2(c * m, s * m);
+}
+
+// Pairs 2 j and 2 j + 1 of a row (a lone last pair is given twice).
+__device__ __forceinline__ void store_turns(float* row, int half, int p0, float2 a, float2 b) {
+  float* dst = row + 2 * p0;
+  if ((half & 1) == 0) {  // whole rows are 16-byte aligned
+    *reinterpret_cast<float4*>(dst) = make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    *reinterpret_cast<float2*>(dst) = a;
+    if (p0 + 1 < half) *reinterpret_cast<float2*>(dst + 2) = b;
+  }
+}
+
+// Thread (r, j): pairs 2 j and 2 j + 1 of rows r, r + step, ...
 __global__ void __launch_bounds__(kTableThreads)
 rope_table_kernel(RopeFreqs f, int rows, const int32_t* __restrict__ pos, float* __restrict__ table) {
   const int hp = (f.half + 1) / 2;  // threads per row
   const int per = kTableThreads / hp;
   const int r0 = threadIdx.x / hp, j = threadIdx.x % hp;
   if (r0 >= per) return;
-  const int p0 = 2 * j, p1 = min(2 * j + 1, f.half - 1);  // a lone last pair is computed twice
+  const int p0 = 2 * j, p1 = min(2 * j + 1, f.half - 1);
   const int a0 = p0 / f.n, a1 = p1 / f.n;
   const double f0 = f.turns[p0 % f.n], f1 = f.turns[p1 % f.n];
   for (long long r = (long long)blockIdx.x * per + r0; r < rows; r += (long long)gridDim.x * per) {
-    int x0, x1;
-    if (pos != nullptr) {
-      x0 = pos[r * f.axes + a0];
-      x1 = pos[r * f.axes + a1];
-    } else if (f.axes == 1) {
-      x0 = x1 = (int)r;
-    } else {
-      const int x = (int)even_bits((uint32_t)r), y = (int)even_bits((uint32_t)r >> 1);
-      x0 = a0 ? y : x;
-      x1 = a1 ? y : x;
-    }
-    const double t0 = (double)x0 * f0, t1 = (double)x1 * f1;
-    float s0, c0, s1, c1;
-    sincospif(2.0f * (float)(t0 - rint(t0)), &s0, &c0);
-    sincospif(2.0f * (float)(t1 - rint(t1)), &s1, &c1);
-    float* dst = table + (r * f.half + p0) * 2;
-    if ((f.half & 1) == 0) {  // whole rows are 16-byte aligned
-      *reinterpret_cast<float4*>(dst) = make_float4(c0 * f.m, s0 * f.m, c1 * f.m, s1 * f.m);
-    } else {
-      *reinterpret_cast<float2*>(dst) = make_float2(c0 * f.m, s0 * f.m);
-      if (p0 + 1 < f.half) *reinterpret_cast<float2*>(dst + 2) = make_float2(c1 * f.m, s1 * f.m);
-    }
+    const int x0 = pos != nullptr ? pos[r * f.axes + a0] : (int)r, x1 = pos != nullptr ? pos[r * f.axes + a1] : (int)r;
+    store_turns(table + r * f.half * 2, f.half, p0, turn_of(x0, f0, f.m), turn_of(x1, f1, f.m));
+  }
+}
+
+// Two axes, positions from the Z-order: 256 consecutive tokens are a square of
+// 16 x 16 pixels, so a CTA forms the turns of its 16 + 16 coordinates and
+// writes each 16 times (65536 rows, rot_dim 64: 13 us computing every entry).
+constexpr int kSquare = 256;
+__global__ void __launch_bounds__(kTableThreads)
+rope_table_square_kernel(RopeFreqs f, int rows, float* __restrict__ table) {
+  __shared__ float2 turns[2][16][kMaxRopeFreqs / 2];  // axis, coordinate, frequency
+  const int r0 = blockIdx.x * kSquare;
+  const int x0 = (int)even_bits((uint32_t)r0), y0 = (int)even_bits((uint32_t)r0 >> 1);
+  for (int i = threadIdx.x; i < 32 * f.n; i += kTableThreads) {
+    const int k = i / f.n, w = i - k * f.n;
+    turns[k >> 4][k & 15][w] = turn_of((k < 16 ? x0 : y0) + (k & 15), f.turns[w], f.m);
+  }
+  __syncthreads();
+  const int hp = (f.half + 1) / 2;
+  for (int i = threadIdx.x; i < kSquare * hp; i += kTableThreads) {
+    const int r = i / hp, p0 = 2 * (i - r * hp), p1 = min(p0 + 1, f.half - 1);
+    if (r0 + r >= rows) return;
+    const int c[2] = {(int)even_bits((uint32_t)r), (int)even_bits((uint32_t)r >> 1)};
+    const int a0 = p0 >= f.n, a1 = p1 >= f.n;
+    store_turns(table + (size_t)(r0 + r) * f.half * 2, f.half, p0, turns[a0][a0 ? c[1] : c[0]][p0 - a0 * f.n],
+                turns[a1][a1 ? c[1] : c[0]][p1 - a1 * f.n]);
   }
 }
 
@@ -291,19 +315,23 @@ __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_
 template <int n>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
-template <typename T, int D>
+template <typename T, int D, bool kFew>
 struct PoolShape {
   static constexpr int kThreads = 16 * D / (2 * Vec16<T>::N);
   // a thread's part of a row: two chunks of Q and of K, its pairs' turns
   static constexpr int kTurns = Vec16<T>::N * 8, kPart = 64 + kTurns;
-  static constexpr int kDepth = kThreads <= 64 ? 4 : 512 / kThreads;  // rows ahead
+  // rows ahead: what hides the latency with several CTAs an SM (32 KB a CTA;
+  // 64 KB measured 174 us against 165 at 256x256 pixels), or, with few CTAs in
+  // all, as many as fit
+  static constexpr int kFit = (232448 - 2 * 16 * D * 4) / (kPart * kThreads);
+  static constexpr int kDepth = kFew ? (kFit < kBlock ? kFit : kBlock) : (kThreads <= 64 ? 4 : 512 / kThreads);
   static constexpr int kSmem = kDepth * kPart * kThreads + 2 * 16 * D * 4;
 };
 
-template <typename T, int D, bool kInterleaved>
-__global__ void __launch_bounds__(PoolShape<T, D>::kThreads)
+template <typename T, int D, bool kInterleaved, bool kFew>
+__global__ void __launch_bounds__(PoolShape<T, D, kFew>::kThreads)
 rope_pool_kernel(RopeParams p, PoolParams o) {
-  using P = PoolShape<T, D>;
+  using P = PoolShape<T, D, kFew>;
   constexpr int VEC = Vec16<T>::N;
   constexpr int SL = D / (2 * VEC);  // slots per row
   constexpr int kRow = D / VEC;      // chunks of a row
@@ -429,27 +457,34 @@ rope_pool_kernel(RopeParams p, PoolParams o) {
   }
 }
 
-template <typename T, int D, bool kInterleaved>
-cudaError_t launch_rope_pool_as(const RopeParams& p, const PoolParams& o, cudaStream_t s) {
-  using P = PoolShape<T, D>;
-  const int n1 = o.N / kBlock;
-  const long long blocks = (long long)((n1 + 15) / 16) * o.BH * (o.L >= 2 ? 2 : 1);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<T, D, kInterleaved>,
+template <typename T, int D, bool kInterleaved, bool kFew>
+cudaError_t launch_rope_pool_as(const RopeParams& p, const PoolParams& o, long long blocks, cudaStream_t s) {
+  using P = PoolShape<T, D, kFew>;
+  const cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<T, D, kInterleaved, kFew>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  rope_pool_kernel<T, D, kInterleaved><<<(unsigned)blocks, P::kThreads, P::kSmem, s>>>(p, o);
+  rope_pool_kernel<T, D, kInterleaved, kFew><<<(unsigned)blocks, P::kThreads, P::kSmem, s>>>(p, o);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_rope_pool_typed(const RopeParams& p, const PoolParams& o, cudaStream_t s) {
-  return p.interleaved ? launch_rope_pool_as<T, D, true>(p, o, s) : launch_rope_pool_as<T, D, false>(p, o, s);
+  const long long blocks = (long long)((o.N / kBlock + 15) / 16) * o.BH * (o.L >= 2 ? 2 : 1);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (blocks <= kSms)
+    return p.interleaved ? launch_rope_pool_as<T, D, true, true>(p, o, blocks, s)
+                         : launch_rope_pool_as<T, D, false, true>(p, o, blocks, s);
+  return p.interleaved ? launch_rope_pool_as<T, D, true, false>(p, o, blocks, s)
+                       : launch_rope_pool_as<T, D, false, false>(p, o, blocks, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeFreqs& f, int rows, const int32_t* pos, float* table, cudaStream_t s) {
+  if (pos == nullptr && f.axes == 2) {
+    rope_table_square_kernel<<<(rows - 1) / kSquare + 1, kTableThreads, 0, s>>>(f, rows, table);
+    return cudaGetLastError();
+  }
   const int per = kTableThreads / ((f.half + 1) / 2);
   long long blocks = ((long long)rows + per - 1) / per;
   if (blocks > 16LL * kSms) blocks = 16LL * kSms;
