@@ -315,23 +315,23 @@ __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_
 template <int n>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
-template <typename T, int D, bool kFew>
+template <typename T, int D>
 struct PoolShape {
   static constexpr int kThreads = 16 * D / (2 * Vec16<T>::N);
   // a thread's part of a row: two chunks of Q and of K, its pairs' turns
   static constexpr int kTurns = Vec16<T>::N * 8, kPart = 64 + kTurns;
-  // rows ahead: what hides the latency with several CTAs an SM (32 KB a CTA;
-  // 64 KB measured 174 us against 165 at 256x256 pixels), or, with few CTAs in
-  // all, as many as fit
-  static constexpr int kFit = (232448 - 2 * 16 * D * 4) / (kPart * kThreads);
-  static constexpr int kDepth = kFew ? (kFit < kBlock ? kFit : kBlock) : (kThreads <= 64 ? 4 : 512 / kThreads);
+  // rows ahead: what hides the latency with several CTAs an SM.  At 256x256
+  // pixels (64 threads): three 166 us, four 165, five 171, eight 174, sixteen
+  // 302.  With a CTA an SM or fewer, every row that fits in flight gains
+  // nothing (10.3 us with four, 10.8 with all; 144 CTAs, bf16, D = 64).
+  static constexpr int kDepth = kThreads <= 64 ? 4 : 512 / kThreads;
   static constexpr int kSmem = kDepth * kPart * kThreads + 2 * 16 * D * 4;
 };
 
-template <typename T, int D, bool kInterleaved, bool kFew>
-__global__ void __launch_bounds__(PoolShape<T, D, kFew>::kThreads)
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(PoolShape<T, D>::kThreads)
 rope_pool_kernel(RopeParams p, PoolParams o) {
-  using P = PoolShape<T, D, kFew>;
+  using P = PoolShape<T, D>;
   constexpr int VEC = Vec16<T>::N;
   constexpr int SL = D / (2 * VEC);  // slots per row
   constexpr int kRow = D / VEC;      // chunks of a row
@@ -457,13 +457,13 @@ rope_pool_kernel(RopeParams p, PoolParams o) {
   }
 }
 
-template <typename T, int D, bool kInterleaved, bool kFew>
+template <typename T, int D, bool kInterleaved>
 cudaError_t launch_rope_pool_as(const RopeParams& p, const PoolParams& o, long long blocks, cudaStream_t s) {
-  using P = PoolShape<T, D, kFew>;
-  const cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<T, D, kInterleaved, kFew>,
+  using P = PoolShape<T, D>;
+  const cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<T, D, kInterleaved>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  rope_pool_kernel<T, D, kInterleaved, kFew><<<(unsigned)blocks, P::kThreads, P::kSmem, s>>>(p, o);
+  rope_pool_kernel<T, D, kInterleaved><<<(unsigned)blocks, P::kThreads, P::kSmem, s>>>(p, o);
   return cudaGetLastError();
 }
 
@@ -471,11 +471,8 @@ template <typename T, int D>
 cudaError_t launch_rope_pool_typed(const RopeParams& p, const PoolParams& o, cudaStream_t s) {
   const long long blocks = (long long)((o.N / kBlock + 15) / 16) * o.BH * (o.L >= 2 ? 2 : 1);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (blocks <= kSms)
-    return p.interleaved ? launch_rope_pool_as<T, D, true, true>(p, o, blocks, s)
-                         : launch_rope_pool_as<T, D, false, true>(p, o, blocks, s);
-  return p.interleaved ? launch_rope_pool_as<T, D, true, false>(p, o, blocks, s)
-                       : launch_rope_pool_as<T, D, false, false>(p, o, blocks, s);
+  return p.interleaved ? launch_rope_pool_as<T, D, true>(p, o, blocks, s)
+                       : launch_rope_pool_as<T, D, false>(p, o, blocks, s);
 }
 
 }  // namespace
