@@ -70,14 +70,27 @@ rope_table_kernel(RopeFreqs f, int rows, const int32_t* __restrict__ pos, float*
   const int a0 = p0 / f.n, a1 = p1 / f.n;
   const double f0 = f.turns[p0 % f.n], f1 = f.turns[p1 % f.n];
   for (long long r = (long long)blockIdx.x * per + r0; r < rows; r += (long long)gridDim.x * per) {
-    const int x0 = pos != nullptr ? pos[r * f.axes + a0] : (int)r, x1 = pos != nullptr ? pos[r * f.axes + a1] : (int)r;
+    int x0, x1;
+    if (pos != nullptr) {
+      x0 = pos[r * f.axes + a0];
+      x1 = pos[r * f.axes + a1];
+    } else if (f.axes == 2) {  // Z-order
+      x0 = (int)even_bits((uint32_t)r >> a0);
+      x1 = (int)even_bits((uint32_t)r >> a1);
+    } else {
+      x0 = x1 = (int)r;
+    }
     store_turns(table + r * f.half * 2, f.half, p0, turn_of(x0, f0, f.m), turn_of(x1, f1, f.m));
   }
 }
 
 // Two axes, positions from the Z-order: 256 consecutive tokens are a square of
 // 16 x 16 pixels, so a CTA forms the turns of its 16 + 16 coordinates and
-// writes each 16 times (65536 rows, rot_dim 64: 13 us computing every entry).
+// writes each 16 times.  Chosen where more than half of the SMs have a square: its coordinates
+// come before its first store, which only other CTAs can cover.  Computing every
+// entry against this, us: rot_dim 64, 256 rows 3.0 and 5.2, 16384 rows 5.5 and
+// 5.6, 65536 rows 9.9 and 7.1; rot_dim 128, 3.5 and 8.6, 8.6 and 8.8, 14.7 and
+// 12.6.
 constexpr int kSquare = 256;
 __global__ void __launch_bounds__(kTableThreads)
 rope_table_square_kernel(RopeFreqs f, int rows, float* __restrict__ table) {
@@ -478,7 +491,7 @@ cudaError_t launch_rope_pool_typed(const RopeParams& p, const PoolParams& o, cud
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeFreqs& f, int rows, const int32_t* pos, float* table, cudaStream_t s) {
-  if (pos == nullptr && f.axes == 2) {
+  if (pos == nullptr && f.axes == 2 && (rows - 1) / kSquare >= kSms / 2) {
     rope_table_square_kernel<<<(rows - 1) / kSquare + 1, kTableThreads, 0, s>>>(f, rows, table);
     return cudaGetLastError();
   }

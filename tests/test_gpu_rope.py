@@ -238,3 +238,15 @@ def test_rope_in_a_graph_and_on_another_stream():
     torch.cuda.synchronize()
     for t, w in zip((oq, ok, buf.pq[1], buf.pk[2], buf.pv[2]), want):
         assert torch.equal(t, w)
+
+
+@pytest.mark.parametrize("rot", [32, 64, 128])
+@pytest.mark.parametrize("rows", [1, 255, 257, 18944, 18945, 37901, 65536])
+def test_table_zorder_equals_positions(rows, rot):
+    """The Z-order's table, computed entry by entry or by squares, is the one of the same positions, bit for bit."""
+    i = torch.arange(rows, dtype=torch.int64, device="cuda")
+    pos = torch.stack([sum(((i >> (2 * b + a)) & 1) << b for b in range(8)) for a in range(2)], 1).int()
+    rope = llsa.make_rope(rot, axes=2)
+    a, b = _table(rope, rows, None, rot // 2), _table(rope, rows, pos.contiguous(), rot // 2)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
