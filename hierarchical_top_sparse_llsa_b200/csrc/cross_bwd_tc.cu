@@ -19,8 +19,9 @@
 // c is what the item's first 16 keys tell of Delta: their part of the sum, and
 // their mean for the probability that the other keys have.  It takes off what
 // the values have in common, so the rounding of P (dP - c) to bf16 is about
-// that of dS, and all of it is exact in c.  (Delta from the stored O would carry O's rounding to bf16, which
-// the keys' common part lifts above the gradient where many keys share a row.)
+// that of dS, and all of it is exact in c.  (Delta from the stored O would carry
+// O's rounding to bf16, which the keys' common part lifts above the gradient
+// where many keys share a row: dQ was up to 7.2e-3 off.)
 // A query that sees one key alone has dS = 0: P is 1 whatever the score.
 //
 // S and dP have kStages stages in tensor memory, each with a group of four
@@ -38,6 +39,10 @@
 // The second pass cuts all its (key tile, query tile) pairs into equal runs,
 // one per SM; a key tile that several SMs share is summed by a last kernel, in
 // a fixed order.  The first pass cuts the keys where there are few rows.
+// 32768 queries x 16 heads x 256 keys, D = 64: 106 us and 83 us, the tensor
+// cores busy for 34% and 51%, the special-function units for 37% and 46%.  With
+// row work, MMAs and loads left out 63% and 47% of the cycles remained: the
+// chain of waits (scores, row work, products, scores) is the largest part.
 // Every wait is bounded; a time-out is reported as LLSA_DEV_TIMEOUT.
 
 #include <math.h>
