@@ -105,6 +105,10 @@ bool spans_apart(const Span* s, int n, int outs) {
   return true;
 }
 
+Span table_span(const llsa_rope_desc* r, const float* table, int rows) {
+  return {table, (size_t)rows * r->rot_dim * sizeof(float)};
+}
+
 RopeParams rope_params(const llsa_rope_desc* r, int B, int H, int N, int D, const float* table, int table_rows) {
   RopeParams p;
   memset(&p, 0, sizeof(p));
@@ -257,6 +261,8 @@ int llsa_rope_table(const llsa_rope_desc* rope, int rows, const int32_t* pos, fl
   const int st = check_rope(rope);
   if (st != LLSA_OK) return st;
   if (rows < 1 || table == nullptr || !aligned(table, 16) || !aligned(pos, 4)) return LLSA_ERR_INVALID_ARG;
+  if (spans_meet(table_span(rope, table, rows), {pos, (size_t)rows * rope->axes * sizeof(int32_t)}))
+    return LLSA_ERR_INVALID_ARG;
   return launch_status(launch_rope_table(rope_freqs(rope), rows, pos, table, (cudaStream_t)stream));
 }
 
@@ -279,6 +285,8 @@ int llsa_rope(const llsa_rope_desc* rope, int B, int H, int N, int D, int dtype,
   const void* in[2] = {q, k};
   void* out[2] = {q_out, k_out};
   if (!outputs_apart(in, nt, out, nt, bytes)) return LLSA_ERR_INVALID_ARG;
+  for (int t = 0; t < nt; ++t)
+    if (spans_meet({out[t], bytes}, table_span(rope, table, table_rows))) return LLSA_ERR_INVALID_ARG;
   RopeParams p = rope_params(rope, B, H, N, D, table, table_rows);
   for (int t = 0; t < nt; ++t) {
     p.x[t] = in[t];
@@ -312,6 +320,23 @@ int llsa_rope_pool(const llsa_desc* desc, const llsa_rope_desc* rope, const floa
   const void* in[3] = {q, k, v};
   void* rot[2] = {q_out, k_out};
   if (!outputs_apart(in, 3, rot, 2, bytes)) return LLSA_ERR_INVALID_ARG;
+  // the pyramid apart from itself, the tensors and the table, the rotated tensors from the table
+  Span spans[3 * LLSA_MAX_LEVELS + 6];
+  int n = 0;
+  size_t level = (size_t)desc->B * desc->H * desc->N * desc->D * sizeof(float);
+  for (int l = 1; l <= desc->L; ++l) {
+    level /= kBlock;
+    spans[n++] = {out->q[l], level};
+    spans[n++] = {out->k[l], level};
+    if (l >= 2) spans[n++] = {out->v[l], level};
+  }
+  const int levels = n;
+  const Span tab = table_span(rope, table, table_rows);
+  spans[n++] = tab;
+  for (const void* ptr : {q, k, v, (const void*)q_out, (const void*)k_out}) spans[n++] = {ptr, bytes};
+  if (!spans_apart(spans, n, levels)) return LLSA_ERR_INVALID_ARG;
+  for (const void* ptr : rot)
+    if (spans_meet({ptr, bytes}, tab)) return LLSA_ERR_INVALID_ARG;
   RopeParams p = rope_params(rope, desc->B, desc->H, desc->N, desc->D, table, table_rows);
   PoolParams o;
   memset(&o, 0, sizeof(o));

@@ -413,7 +413,8 @@ typedef struct {
  *   pos: int32 [rows, axes], any values, or NULL: row r is token r, whose
  *   position is r (axes = 1) or its pixel (x, y) in Z-order (axes = 2; axis 0
  *   is x, from the even bits of r, axis 1 is y, from the odd bits).
- *   rows >= 1.  The layout and D play no part in the table.
+ *   rows >= 1.  The layout and D play no part in the table, which may not
+ *   overlap pos (else LLSA_ERR_INVALID_ARG).
  */
 LLSA_API int llsa_rope_table(const llsa_rope_desc* rope, int rows, const int32_t* pos, float* table, void* stream);
 
@@ -441,7 +442,8 @@ LLSA_API int llsa_rope(const llsa_rope_desc* rope, int B, int H, int N, int D, i
  * registers.  Writes exactly what the two calls write, bit for bit.
  *   desc, out: as llsa_pool takes them.  table, table_rows, q, k, q_out,
  *   k_out: as llsa_rope takes them (all required; q_out may be q, k_out may be
- *   k).  v: [B, H, N, D], read.
+ *   k).  v: [B, H, N, D], read.  The levels written overlap neither each other
+ *   nor anything else (else LLSA_ERR_INVALID_ARG).
  */
 LLSA_API int llsa_rope_pool(const llsa_desc* desc, const llsa_rope_desc* rope, const float* table, int table_rows,
                             const void* q, const void* k, const void* v, void* q_out, void* k_out,

@@ -118,6 +118,54 @@ def test_rope_pool_refusals(kw, status):
     assert rope_pool(**kw) == status
 
 
+def _apart_pyramid(**kw):
+    p = llsa.LlsaPyramid()
+    for i, (l, n) in enumerate((l, n) for l in (1, 2) for n in "qkv"):
+        getattr(p, n)[l] = _apart(10 + i)
+    for name, ptr in kw.items():
+        getattr(p, name[0])[int(name[1])] = ptr
+    return p
+
+
+# Outputs over the table or the pyramid.  Q has 1024 rows x 2 heads x 64 bf16
+# (256 KB), the table 1024 x 32 pairs (256 KB), level 1 of Q 32 KB.
+@pytest.mark.parametrize("kw,pyr", [
+    (dict(q_out=A + 1024), {}),
+    (dict(k_out=A + 256 * 1024 - 16), {}),
+    ({}, dict(q1=A)),
+    ({}, dict(q1=_apart(0) + 256)),
+    ({}, dict(k2=_apart(1))),
+    ({}, dict(v2=_apart(2) + 16)),
+    ({}, dict(q1=_apart(3) + 4096)),
+    ({}, dict(v2=_apart(4))),
+    ({}, dict(k1=_apart(10) + 32 * 1024 - 16)),
+    ({}, dict(q2=_apart(11))),
+])
+def test_rope_pool_refuses_overlap(kw, pyr):
+    a = dict(table=A, q=_apart(0), k=_apart(1), v=_apart(2), q_out=_apart(3), k_out=_apart(4))
+    a.update(kw)
+    d = llsa.make_desc(1, 2, 1024, 64, 2, 4, llsa.BF16)
+    st = llsa.llsa_rope_pool(d, llsa.make_rope(64), a["table"], 1024, a["q"], a["k"], a["v"], a["q_out"], a["k_out"],
+                             _apart_pyramid(**pyr), check=False)
+    assert st == llsa.ERR_INVALID_ARG
+
+
+def test_rope_table_refuses_pos_over_the_table():
+    r = llsa.make_rope(64, axes=2)  # 10 rows: 2560 bytes, and 80 of positions
+    for pos in (A, A + 2556, A - 76):
+        assert llsa.llsa_rope_table(r, 10, pos, A, check=False) == llsa.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("out", [dict(q_out=A + 16), dict(k_out=A + 12672 - 16)])
+def test_rope_refuses_outputs_over_the_table(out):
+    """99 rows of 32 pairs: 25344 bytes a table, 12672 of them of rot_dim 32."""
+    a = dict(q_out=_apart(2), k_out=_apart(3))
+    a.update(out)
+    st = llsa.llsa_rope(llsa.make_rope(32), 1, 2, 99, 64, llsa.BF16, A, 99, _apart(0), _apart(1), a["q_out"],
+                        a["k_out"], 0, check=False)
+    assert st == llsa.ERR_INVALID_ARG
+
+
 def desc(**kw):
     a = dict(B=2, H=4, Hkv=2, N=100, S=77, D=64, dtype=llsa.BF16)
     a.update(kw)
