@@ -167,3 +167,72 @@ def test_block_chain(dtype, code):
     torch.cuda.synchronize()
     for n, t in {**grads, "co": co, "o": o}.items():
         assert torch.equal(t, want[n]), n
+
+
+def _banded(shape, dtype, band=4096):
+    """A tensor inside a larger one of the value 7, and a check that the rest still has it."""
+    n = math.prod(shape)
+    whole = torch.full((n + 2 * band,), 7.0, dtype=dtype, device="cuda")
+    inner = whole[band:band + n].view(shape)
+    return inner, lambda: bool((whole[:band] == 7).all()) and bool((whole[band + n:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(2, 6, 2, 131, 77, 64), (1, 2, 1, 1, 2049, 128), (3, 2, 2, 515, 1, 64),
+                                   (1, 4, 4, 1023, 333, 128)], ids=str)
+def test_replay_on_new_inputs_writes_outputs_alone(shape, dtype):
+    """A captured forward and backward without a status word, replayed after
+    its inputs changed: the values of the new inputs, and nothing around the
+    outputs or the workspace is written."""
+    B, H, Hkv, N, S, D = shape
+    x, y = make(*shape, dtype, seed=31), make(*shape, dtype, seed=32)
+    t = x["q"].dtype
+    desc = llsa.make_cross(B, H, Hkv, N, S, D, llsa.BF16 if dtype == "bf16" else llsa.F32)
+    fb, bb = llsa.llsa_cross_fwd_workspace_bytes(desc), llsa.llsa_cross_bwd_workspace_bytes(desc)
+    bands = {n: _banded(x[n[1:] if n != "o" else "q"].shape, t) for n in ("o", "dq", "dk", "dv")}
+    bands["lse"] = _banded((B, H, N), torch.float32)
+    bands["ws"] = _banded((max(fb, bb, 256) // 4,), torch.float32)
+    out = {n: b[0] for n, b in bands.items()}
+
+    def step():
+        s = _stream()
+        llsa.llsa_cross_attn_fwd(desc, _p(x["q"]), _p(x["k"]), _p(x["v"]), None, None, _p(out["o"]), None,
+                                 _p(out["lse"]), _p(out["ws"]), fb, None, s)
+        llsa.llsa_cross_attn_bwd(desc, _p(x["q"]), _p(x["k"]), _p(x["v"]), None, None, _p(out["o"]), None,
+                                 _p(out["lse"]), _p(x["do"]), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
+                                 _p(out["ws"]), bb, None, s)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for n in x:
+        x[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    want = run(y)
+    for n, w in want.items():
+        assert torch.equal(out[n], w), n
+    for n, (_, whole) in bands.items():
+        assert whole(), n
+    check(y, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,rot,layout", [(64, 64, 0), (64, 20, 0), (128, 128, 1), (128, 6, 1)])
+def test_rotation_writes_outputs_alone(D, rot, layout, dtype):
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    code = llsa.BF16 if dtype == "bf16" else llsa.F32
+    B, H, N = 2, 3, 77
+    rope = llsa.make_rope(rot, layout=layout)
+    table, tab_ok = _banded((N, rot // 2, 2), torch.float32)
+    llsa.llsa_rope_table(rope, N, None, _p(table), _stream())
+    g = torch.Generator(device="cuda").manual_seed(33)
+    q, k = (torch.randn(B, H, N, D, generator=g, device="cuda").to(t) for _ in "qk")
+    (qo, q_ok), (ko, k_ok) = _banded(q.shape, t), _banded(k.shape, t)
+    llsa.llsa_rope(rope, B, H, N, D, code, _p(table), N, _p(q), _p(k), _p(qo), _p(ko), 0, _stream())
+    torch.cuda.synchronize()
+    assert tab_ok() and q_ok() and k_ok()
+    for x, got in ((q, qo), (k, ko)):
+        y, mag = bt.rotate(x.double(), table.double(), rot, bool(layout))
+        bt.within(got, y, bt.rotate_bound(y, mag, dtype == "bf16"), "rotation")
