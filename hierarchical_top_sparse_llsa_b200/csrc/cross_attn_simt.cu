@@ -32,11 +32,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 inline int tiles_of(int n, int t = kT) { return n / t + (n % t != 0); }
 
 // rows r < nrows of src [.., D] (kept where keep is null or keep[r] != 0) into
-// ROWS dst rows of LD floats; the others as zeros
-template <int D, int LD, int THREADS, int ROWS>
-__device__ __forceinline__ void load_rows(float* dst, const void* src, int nrows, const uint8_t* keep) {
+// `rows` dst rows of LD floats; the others as zeros
+template <int D, int LD, int THREADS>
+__device__ __forceinline__ void load_rows(float* dst, const void* src, int nrows, const uint8_t* keep, int rows = kT) {
 #pragma unroll 4
-  for (int e = threadIdx.x; e < ROWS * (D / 4); e += THREADS) {
+  for (int e = threadIdx.x; e < rows * (D / 4); e += THREADS) {
     const int r = e / (D / 4), c = (e % (D / 4)) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nrows && (keep == nullptr || keep[r] != 0))
@@ -102,6 +102,12 @@ __device__ __forceinline__ void dot_tile(float (&acc)[R][4], const float* a, con
 
 constexpr int kLP = kT + 4;  // row length of the probability tiles
 
+// Rows that the forward's key tiles hold: what dot_tile and the product read of
+// a short sequence's only tile, so that more CTAs fit on an SM (9 heads of 29127
+// queries, us, against 64 rows always: D = 128, one key 158 and 166, 16 keys 194
+// and 205, 32 keys 258 and 268; D = 64, 90 and 94, 108 and 113, 144 and 148).
+__host__ __device__ inline int key_rows(int S) { return S > 32 ? kT : (S > 16 ? 32 : 16); }
+
 // ----------------------------------------------------------------- forward
 // R query rows a thread, 8 R a tile
 template <int D, int R>
@@ -112,8 +118,9 @@ cross_fwd_simt(CrossParams p, int qtiles) {
   __shared__ uint8_t keep[kT];
   constexpr int kQ = 8 * R;
   float* Q = smf;             // [kQ][LD]
-  float* K = Q + kQ * LD;     // [64][LD], then P [kQ][kLP]
-  float* V = K + kT * LD;     // [64][D]
+  const int kr = key_rows(p.S);
+  float* K = Q + kQ * LD;     // [kr][LD], then P [kQ][kLP]
+  float* V = K + max(kr * LD, kQ * kLP);  // [kr][D]
   float* P = K;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   long long id = blockIdx.x;
@@ -130,7 +137,7 @@ cross_fwd_simt(CrossParams p, int qtiles) {
   const int kt0 = (int)((long long)ktiles * split / p.nks), kt1 = (int)((long long)ktiles * (split + 1) / p.nks);
   const float sc2 = p.scale * kLog2e;
 
-  load_rows<D, LD, kFwdThreads, kQ>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
+  load_rows<D, LD, kFwdThreads>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr, kQ);
   float o[R][D / 16];
   float m[R], l[R];
 #pragma unroll
@@ -146,8 +153,8 @@ cross_fwd_simt(CrossParams p, int qtiles) {
     load_keep(keep, p, b, k0, len);
     __syncthreads();
     const int nk = min(kT, p.S - k0);
-    load_rows<D, LD, kFwdThreads, kT>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep);
-    load_rows<D, D, kFwdThreads, kT>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, LD, kFwdThreads>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep, kr);
+    load_rows<D, D, kFwdThreads>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep, kr);
     __syncthreads();
     float s[R][4];
     dot_tile<D, R>(s, Q, K, nk, ty, tx);
@@ -369,8 +376,8 @@ __device__ __forceinline__ void dq_tile(const CrossParams& p, int qtiles, long l
   const int ktiles = (len + kT - 1) / kT;
   const int kt0 = (int)((long long)ktiles * split / p.nks), kt1 = (int)((long long)ktiles * (split + 1) / p.nks);
   const bool one = sees_one(p, b, len);
-  load_rows<D, LD, kBwdThreads, kT>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
-  load_rows<D, LD, kBwdThreads, kT>(dO, static_cast<const float*>(p.dout) + row0 * D, nq, nullptr);
+  load_rows<D, LD, kBwdThreads>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
+  load_rows<D, LD, kBwdThreads>(dO, static_cast<const float*>(p.dout) + row0 * D, nq, nullptr);
   __syncthreads();
   load_side<D>(lse2, del, dO, p, row0, nq);
   float acc[4][D / 16];
@@ -383,8 +390,8 @@ __device__ __forceinline__ void dq_tile(const CrossParams& p, int qtiles, long l
     __syncthreads();
     load_keep(keep, p, b, k0, len);
     __syncthreads();
-    load_rows<D, LD, kBwdThreads, kT>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep);
-    load_rows<D, LD, kBwdThreads, kT>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, LD, kBwdThreads>(K, static_cast<const float*>(p.k) + (kvrow + k0) * D, nk, keep);
+    load_rows<D, LD, kBwdThreads>(V, static_cast<const float*>(p.v) + (kvrow + k0) * D, nk, keep);
     __syncthreads();
     p_and_ds<D>(Q, K, dO, V, P, dS, lse2, del, keep, p.scale * kLog2e, one, nk, ty, tx);
     __syncwarp();  // a dS row is written and read by one half warp
@@ -444,8 +451,8 @@ __device__ __forceinline__ void dkv_tile(const CrossParams& p, int qtiles, int k
   const bool one = sees_one(p, b, len);
   load_keep(keep, p, b, k0, len);
   __syncthreads();
-  load_rows<D, LD, kBwdThreads, kT>(K, static_cast<const float*>(p.k) + kvrow * D, nk, keep);
-  load_rows<D, LD, kBwdThreads, kT>(V, static_cast<const float*>(p.v) + kvrow * D, nk, keep);
+  load_rows<D, LD, kBwdThreads>(K, static_cast<const float*>(p.k) + kvrow * D, nk, keep);
+  load_rows<D, LD, kBwdThreads>(V, static_cast<const float*>(p.v) + kvrow * D, nk, keep);
   float ak[4][D / 16], av[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -457,8 +464,8 @@ __device__ __forceinline__ void dkv_tile(const CrossParams& p, int qtiles, int k
     const int q0 = qt * kT, nq = min(kT, p.N - q0);
     const size_t row0 = (size_t)bh * p.N + q0;
     __syncthreads();
-    load_rows<D, LD, kBwdThreads, kT>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
-    load_rows<D, LD, kBwdThreads, kT>(dO, static_cast<const float*>(p.dout) + row0 * D, nq, nullptr);
+    load_rows<D, LD, kBwdThreads>(Q, static_cast<const float*>(p.q) + row0 * D, nq, nullptr);
+    load_rows<D, LD, kBwdThreads>(dO, static_cast<const float*>(p.dout) + row0 * D, nq, nullptr);
     __syncthreads();
     load_side<D>(lse2, del, dO, p, row0, nq);
     __syncthreads();
@@ -559,7 +566,8 @@ cudaError_t fwd_typed(const CrossParams& p, cudaStream_t s) {
   const int qt = tiles_of(p.N, 8 * R);
   const long long blocks = (long long)p.B * p.H * p.nks * qt;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)((8 * R + kT) * (D + 4) + kT * D) * sizeof(float);
+  const int kr = key_rows(p.S), kq = 8 * R;
+  const size_t smem = (size_t)(kq * (D + 4) + max(kr * (D + 4), kq * kLP) + kr * D) * sizeof(float);
   cudaError_t e = allow_smem(cross_fwd_simt<D, R>, smem);
   if (e != cudaSuccess) return e;
   cross_fwd_simt<D, R><<<(unsigned)blocks, kFwdThreads, smem, s>>>(p, qt);
