@@ -252,7 +252,9 @@ cross_combine_kernel(CrossParams p) {
 #pragma unroll 4
   for (int z = kWarps == 1 ? 0 : warp; z < p.nks; z += kWarps) {
     const float2 ml = p.part_ml[z * rows + row];
-    if (ml.x == -INFINITY) continue;  // a split without keys: its O may not be written
+    // a split without keys: its O may not be written.  By the sum, for a split
+    // whose scores are all NaN has no maximum either, and must show.
+    if (ml.y == 0.f) continue;
     const float w = exp2f(ml.x - mb);
     l = fmaf(ml.y, w, l);
     const float* src = p.part_o + (z * rows + row) * D + lane * C;

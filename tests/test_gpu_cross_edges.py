@@ -1,0 +1,53 @@
+"""Cross attention on the GPU where its answer hangs on how the work is cut:
+NaN among split keys, no states at all, items without rows for every tile."""
+
+import math
+
+import pytest
+import torch
+
+from test_gpu_cross_attn import check, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+# the keys in one piece, and split over the SMs
+WHOLE_AND_SPLIT = [(1, 2, 2, 300, 40, 64), (1, 2, 2, 300, 40, 128), (1, 2, 1, 5, 3000, 64), (2, 4, 2, 3, 5000, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", WHOLE_AND_SPLIT, ids=str)
+def test_nan_query_shows(shape, dtype):
+    """A NaN query has scores that are all NaN: O and lse of its row are NaN,
+    and no other row's are."""
+    x = make(*shape, dtype, seed=41)
+    clean = run(x, grads=False)
+    x["q"][0, 1, 2, 3] = float("nan")
+    out = run(x, grads=False)
+    for n in ("o", "lse"):
+        assert torch.isnan(out[n][0, 1, 2]).all(), n
+        out[n][0, 1, 2] = clean[n][0, 1, 2]
+        assert torch.equal(out[n], clean[n]), n
+    # and its gradients
+    out = run(x)
+    assert torch.isnan(out["dq"][0, 1, 2]).all()
+    out["dq"][0, 1, 2] = 0
+    assert torch.isfinite(out["dq"]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", WHOLE_AND_SPLIT, ids=str)
+def test_nan_keys_show(shape, dtype):
+    """One NaN state that is seen reaches every query of its heads, also where
+    it is the only one that its split of the keys sees."""
+    B, H, Hkv, N, S, D = shape
+    for at, hide in ((S // 2, False), (S - 1, True)):
+        x = make(*shape, dtype, seed=42)
+        mask = torch.ones(B, S, dtype=torch.uint8, device="cuda")
+        if hide:  # the back half but for the last state
+            mask[:, S // 2 : S - 1] = 0
+        x["k"][0, 0, at, 5] = float("nan")
+        out = run(x, None, mask, grads=False)
+        heads = H // Hkv
+        assert torch.isnan(out["o"][0, :heads]).all() and torch.isnan(out["lse"][0, :heads]).all()
+        assert torch.isfinite(out["o"][0, heads:]).all() and torch.isfinite(out["o"][1:]).all()
