@@ -618,7 +618,8 @@ CrossPlan cross_simt_fwd_plan(long long BH, int N, int S) {
 }
 
 CrossPlan cross_simt_bwd_plan(long long BH, int N, int S) {
-  return {parts_for(BH * tiles_of(N), tiles_of(S)), parts_for(BH * (S > 0 ? tiles_of(S) : 1), tiles_of(N))};
+  if (S == 0) return {1, 1};  // no dK and dV to cut or to join
+  return {parts_for(BH * tiles_of(N), tiles_of(S)), parts_for(BH * tiles_of(S), tiles_of(N))};
 }
 
 cudaError_t launch_cross_fwd_simt(const CrossParams& p, cudaStream_t s) {

@@ -51,3 +51,11 @@ def test_nan_keys_show(shape, dtype):
         heads = H // Hkv
         assert torch.isnan(out["o"][0, :heads]).all() and torch.isnan(out["lse"][0, :heads]).all()
         assert torch.isfinite(out["o"][0, heads:]).all() and torch.isfinite(out["o"][1:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,Hkv,N,D", [(1, 1, 1, 129, 64), (2, 6, 2, 1000, 64), (2, 4, 1, 43, 128), (1, 2, 2, 5000, 128),
+                                         (1, 1, 1, 1, 64)])
+def test_no_states_for_any_number_of_queries(B, H, Hkv, N, D, dtype):
+    out = run(make(B, H, Hkv, N, 0, D, dtype, seed=43))
+    assert (out["o"] == 0).all() and (out["lse"] == -math.inf).all() and (out["dq"] == 0).all()
