@@ -241,12 +241,20 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint32_t turn[C::kPer] = {};   // parity of p_full
     bool pend[C::kPer] = {};
     int pnt = 0;                   // the pending products' 16-key steps
-    bool pfirst = false, plast = false, pfree = false;
-    auto products = [&](int u) {   // O_w (+)= P_w V of the previous step
+    bool pfirst = false, plast = false, pfree = false, held = false;
+    // O_w (+)= P_w V of the previous step.  V is waited for by every issuing
+    // warp at every step, also for tiles without rows: its slots are then freed
+    // only after it has been seen, and who waits for S of the next step knows
+    // that V of every step before is there (a barrier tells rounds apart by
+    // parity, so no wait for one may begin before the round before is over).
+    auto products = [&](int u) {
+      if (u == 0 && held) {
+        held = false;
+        if (clean ? !wait(pv_at.at(kv_clean), pv_at.parity) : !wait(pv_at.at(kv_full), pv_at.parity)) return;
+      }
       if (!pend[u]) return;
       pend[u] = false;
       const int w = w0 + u;
-      if (clean ? !wait(pv_at.at(kv_clean), pv_at.parity) : !wait(pv_at.at(kv_full), pv_at.parity)) return;
       if (!wait(p_full + 8 * w, turn[u])) return;
       turn[u] ^= 1u;
       tc_fence_after();
@@ -299,6 +307,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         pfirst = j == 0;
         plast = j == nkt - 1;
         pfree = free;
+        held = true;
         kv.next(2);
       }
       rq.next(nact);

@@ -6,7 +6,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_cross_attn import check, make, run
+import block_testlib as bt
+from test_gpu_cross_attn import make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +60,25 @@ def test_nan_keys_show(shape, dtype):
 def test_no_states_for_any_number_of_queries(B, H, Hkv, N, D, dtype):
     out = run(make(B, H, Hkv, N, 0, D, dtype, seed=43))
     assert (out["o"] == 0).all() and (out["lse"] == -math.inf).all() and (out["dq"] == 0).all()
+
+
+# Items that have rows for one or two of the four query tiles (D = 64) come
+# before items that have them all, at the start of a CTA's run too, with key
+# tiles that fill the ring of slots exactly, nearly, or not
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("N", [520, 700, 1100])
+@pytest.mark.parametrize("S", [40, 330, 384, 390])
+def test_items_without_rows_for_every_tile(S, N, masked):
+    x = make(6, 37, 37, N, S, 64, "bf16", seed=44)
+    lens = mask = None
+    if masked:
+        g = torch.Generator(device="cuda").manual_seed(45)
+        lens = torch.tensor([S, S - 1, S // 2, S, 1, S], dtype=torch.int32, device="cuda")
+        mask = (torch.rand(6, S, generator=g, device="cuda") < 0.7).to(torch.uint8)
+    a = run(x, lens, mask, grads=False)
+    want = bt.cross(x["q"], x["k"], x["v"], lens, mask)
+    for n in ("o", "lse"):
+        bt.within(a[n], *want[n], n)
+    for _ in range(3):
+        b = run(x, lens, mask, grads=False)
+        assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
