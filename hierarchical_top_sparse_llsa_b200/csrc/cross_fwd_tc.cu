@@ -9,9 +9,9 @@
 // 128 of these rows (the M of an MMA) against a range of key tiles; a
 // persistent CTA per SM walks a contiguous range of items.  Warps:
 //   four per query tile: its softmax, one thread per row;
-//   load   TMA loads: Q tiles into a ring of slots, K and V tiles into
-//          another.  Key tiles that fit in the ring are loaded once and stay
-//          for all items of the same keys;
+//   load   TMA loads: Q tiles into a ring of slots for each mma warp, K and V
+//          tiles into another.  Key tiles that fit in the ring are loaded
+//          once and stay for all items of the same keys;
 //   mma    (one for every query tile) issues S_w = Q_w K^T into tensor
 //          memory, and O_w += P_w V with P_w read from tensor memory (over
 //          S_w, which the softmax has read);
@@ -54,7 +54,10 @@ struct Cfg {
   static constexpr int kThreads = (kStore + 1) * 32;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kKvTile = kKeys * D * 2;
-  static constexpr int kQ = (D == 64) ? 8 : 3;          // Q slots
+  // Q slots: a ring of kQr for the tiles of each mma warp, which so waits for
+  // every round of its slots, in order
+  static constexpr int kQ = (D == 64) ? 8 : 3;
+  static constexpr int kQr = kQ / kMmaWarps;
   static constexpr int kKv = (D == 64) ? 12 : 4;        // K and V slots
   static constexpr int kOffKv = kQ * kQTile;
   static constexpr int kEnd = kOffKv + kKv * kKvTile;
@@ -63,7 +66,8 @@ struct Cfg {
 
 template <typename C>
 struct Shared {
-  uint64_t q_full[C::kQ], q_empty[C::kQ], kv_full[C::kKv], kv_empty[C::kKv], kv_clean[C::kKv];
+  uint64_t q_full[C::kMmaWarps][C::kQr], q_empty[C::kMmaWarps][C::kQr];
+  uint64_t kv_full[C::kKv], kv_empty[C::kKv], kv_clean[C::kKv];
   uint64_t s_full[C::kNq], p_full[C::kNq], o_full[C::kNq], o_staged[C::kNq], done;
   uint32_t bits[C::kKv][C::kKeys / 32];  // keys seen, by V slot
   uint32_t tmem_base;
@@ -160,8 +164,8 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     tmem_relinquish();
   } else if (tid == 0) {
     for (int i = 0; i < C::kQ; ++i) {
-      mbar_init(smem_u32(&S.q_full[i]), 1);
-      mbar_init(smem_u32(&S.q_empty[i]), 1);
+      mbar_init(smem_u32(&S.q_full[i / C::kQr][i % C::kQr]), 1);
+      mbar_init(smem_u32(&S.q_empty[i / C::kQr][i % C::kQr]), 1);
     }
     for (int i = 0; i < C::kKv; ++i) {
       mbar_init(smem_u32(&S.kv_full[i]), 1);
@@ -181,17 +185,20 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = uniform(S.tmem_base);
-  auto qslot = [&](uint32_t i) { return base + i * C::kQTile; };
+  // Q slots and their barriers, by ring (the mma warp whose tiles take it) and place
+  auto qslot = [&](int ring, uint32_t i) { return base + (ring * C::kQr + i) * C::kQTile; };
   auto kvslot = [&](uint32_t i) { return base + C::kOffKv + i * C::kKvTile; };
-  const uint32_t q_full = smem_u32(S.q_full), q_empty = smem_u32(S.q_empty), kv_full = smem_u32(S.kv_full),
-                 kv_empty = smem_u32(S.kv_empty), kv_clean = smem_u32(S.kv_clean), s_full = smem_u32(S.s_full),
-                 p_full = smem_u32(S.p_full), o_full = smem_u32(S.o_full), o_staged = smem_u32(S.o_staged);
+  auto q_full = [&](int ring) { return smem_u32(S.q_full[ring]); };
+  auto q_empty = [&](int ring) { return smem_u32(S.q_empty[ring]); };
+  const uint32_t kv_full = smem_u32(S.kv_full), kv_empty = smem_u32(S.kv_empty), kv_clean = smem_u32(S.kv_clean),
+                 s_full = smem_u32(S.s_full), p_full = smem_u32(S.p_full), o_full = smem_u32(S.o_full),
+                 o_staged = smem_u32(S.o_staged);
   auto wait = [&](uint32_t bar, uint32_t parity) { return ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
   FwdItems<C> it(p);
 
   if (warp == C::kLoad) {
     if (lane == 0) {
-      Ring<C::kQ> rq;
+      Ring<C::kQr> rq[C::kMmaWarps];
       Ring<C::kKv> rk;
       // a slot's first round waits for the phase before the first, which is over
       auto load = [&](uint32_t dst, uint32_t half, const CUtensorMap* map, int row, uint32_t full, uint32_t bytes) {
@@ -200,10 +207,12 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int h = 0; h < H; ++h) tma_load_3d(dst + h * half, map, 64 * h, row, it.bk, full);
       };
       auto load_q = [&](int w) {
-        if (ok) ok = mbar_wait(rq.at(q_empty), rq.parity ^ 1u);
+        const int u = w / C::kPer;
+        Ring<C::kQr>& r = rq[u];
+        if (ok) ok = mbar_wait(r.at(q_empty(u)), r.parity ^ 1u);
         if (!ok) return;
-        load(qslot(rq.i), 16384, &tq, it.r0 + 128 * w, rq.at(q_full), C::kQTile);
-        rq.next();
+        load(qslot(u, r.i), 16384, &tq, it.r0 + 128 * w, r.at(q_full(u)), C::kQTile);
+        r.next();
       };
       auto load_kv = [&](const CUtensorMap* map, int j) {
         if (ok) ok = mbar_wait(rk.at(kv_empty), rk.parity ^ 1u);
@@ -216,7 +225,9 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const int n = it.loads() ? it.nkt : 0;
         load_q(0);
         if (n > 0) load_kv(&tk, 0);
-        for (int w = 1; w < it.nact; ++w) load_q(w);
+#pragma unroll
+        for (int w = 1; w < C::kNq; ++w)
+          if (w < it.nact) load_q(w);
         if (n > 0) load_kv(&tv, 0);
         for (int j = 1; j < n && ok; ++j) {
           load_kv(&tk, j);
@@ -225,18 +236,20 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       }
       // no copy may still be landing when the CTA exits: of every slot, the
       // last round that was begun
-      for (int i = 0; i < C::kQ; ++i, rq.next())
-        if (!mbar_wait(rq.at(q_full), rq.parity ^ 1u)) ok = false;
+#pragma unroll
+      for (int u = 0; u < C::kMmaWarps; ++u)
+        for (int i = 0; i < C::kQr; ++i, rq[u].next())
+          if (!mbar_wait(rq[u].at(q_full(u)), rq[u].parity ^ 1u)) ok = false;
       for (int i = 0; i < C::kKv; ++i, rk.next())
         if (!mbar_wait(rk.at(kv_full), rk.parity ^ 1u)) ok = false;
     }
   } else if (warp >= C::kMma && warp < C::kClean) {
     // query tiles w0 .. w0 + kPer - 1; the whole warp walks, one lane issues
-    const int w0 = C::kPer * (warp - C::kMma);
+    const int ring = warp - C::kMma, w0 = C::kPer * ring;
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1, 0);
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), nmaj = smem_desc_sw128(0, kKvHalf, 1024);
     const uint32_t lead = elect_lane();
-    Ring<C::kQ> rq;                // of the item's first query tile
+    Ring<C::kQr> rq;               // of the first of them
     Ring<C::kKv> run, kv, pv_at;   // the run's first tile, this step's K, the pending products' V
     uint32_t turn[C::kPer] = {};   // parity of p_full
     bool pend[C::kPer] = {};
@@ -286,11 +299,11 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
           if (ok) products(u);
           const int w = w0 + u;
           if (!ok || w >= nact) continue;
-          Ring<C::kQ> at = rq;
-          at.next(w);
-          if (j == 0 && !wait(at.at(q_full), at.parity)) continue;
+          Ring<C::kQr> at = rq;
+          at.next(u);
+          if (j == 0 && !wait(at.at(q_full(ring)), at.parity)) continue;
           tc_fence_after();
-          const uint64_t q = desc_at(kmaj, qslot(at.i));
+          const uint64_t q = desc_at(kmaj, qslot(ring, at.i));
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             tc_mma_f16_by(lead, tbase + w * C::kKeys, desc_at(q, (ks >> 2) * 16384 + (ks & 3) * 32),
@@ -310,7 +323,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         held = true;
         kv.next(2);
       }
-      rq.next(nact);
+      rq.next(min(max(nact - w0, 0), C::kPer));
     }
 #pragma unroll
     for (int u = 0; u < C::kPer; ++u)
@@ -352,21 +365,25 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     }
   } else if (warp == C::kStore) {
     if (lane == 0) {
-      Ring<C::kQ> rq;
+      Ring<C::kQr> rq[C::kMmaWarps];
       uint32_t turn = 0;  // parities of o_staged, a bit each
       for (; ok && it.next();) {
         if (it.nkt == 0) continue;
-        for (int w = 0; w < it.nact; ++w, rq.next()) {
+#pragma unroll
+        for (int w = 0; w < C::kNq; ++w) {
+          if (!ok || w >= it.nact) break;
           ok = mbar_wait(o_staged + 8 * w, (turn >> w) & 1u);
           if (!ok) break;
           turn ^= 1u << w;
+          const int u = w / C::kPer;
           if (p.nks == 1) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) tma_store_3d(&to, 64 * h, it.r0 + 128 * w, it.bk, qslot(rq.i) + h * 16384);
+            for (int h = 0; h < H; ++h) tma_store_3d(&to, 64 * h, it.r0 + 128 * w, it.bk, qslot(u, rq[u].i) + h * 16384);
             bulk_commit_group();
             bulk_wait_read_all();
           }
-          mbar_arrive(rq.at(q_empty));
+          mbar_arrive(rq[u].at(q_empty(u)));
+          rq[u].next();
         }
       }
       bulk_wait_all();
@@ -379,11 +396,12 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     const uint32_t ts = trow + (uint32_t)(w * C::kKeys), tO = trow + C::kColO + (uint32_t)w * D;
     const float sc2 = p.scale * kLog2e;
     const uint64_t sc2x2 = f2_make(sc2, sc2);
-    Ring<C::kQ> rq;
+    const int ring = w / C::kPer, w0 = C::kPer * ring;
+    Ring<C::kQr> rq;       // of the first of the ring's tiles
     Ring<C::kKv> run, rv;  // of V
     rv.next();
     uint32_t s_turn = 0, o_turn = 0;
-    Ring<C::kQ> last;      // the slot of this tile's last item
+    Ring<C::kQr> last;     // the slot of this tile's last item
     bool staged = false;
     for (; ok && it.next();) {
       const int row = it.r0 + 128 * w + r;
@@ -405,9 +423,9 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       }
       if (it.loads()) run = rv;
       else rv = run;
-      Ring<C::kQ> at = rq;
-      at.next(w);
-      rq.next(it.nact);
+      Ring<C::kQr> at = rq;
+      at.next(w - w0);
+      rq.next(min(max(it.nact - w0, 0), C::kPer));
       if (w >= it.nact) {
         for (int j = 0; j < it.nkt; ++j) rv.next(2);
         continue;
@@ -487,7 +505,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       tc_fence_after();
       const bool valid = row < it.R;
       const float inv = l != 0.f ? 1.f / l : 0.f;  // 0 without keys; NaN stays NaN
-      unsigned char* stage = sm + (qslot(at.i) - base);
+      unsigned char* stage = sm + (qslot(ring, at.i) - base);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -522,7 +540,7 @@ cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
       fence_proxy_async_smem();  // generic writes -> TMA store
       tc_fence_before();
       // the store warp has taken the last one, else this phase could pass it by
-      if (staged && !wait(last.at(q_empty), last.parity)) break;
+      if (staged && !wait(last.at(q_empty(ring)), last.parity)) break;
       last = at;
       staged = true;
       mbar_arrive(o_staged + 8 * w);
