@@ -1,0 +1,113 @@
+"""Gradients of cross attention on the GPU, by the norm of their error.
+
+The element bounds of block_testlib add up every rounding in absolute value and
+take Delta from the stored O, so they are wide where many keys or queries share
+a sum.  These tests hold the whole of a gradient to the size that its roundings
+have when they are independent of one another.
+
+bf16: a rounding to bf16 is off by R of the value, root mean square: half a step
+(2^-8 of the power of two below the value) uniformly, sqrt(1/3), over mantissas
+that are spread evenly by logarithm, sqrt(3/4 / (2 ln 2)).  With P and dS rounded
+for the products and the result rounded once,
+    |err dV|^2 = R^2 (sum_ij P_ij^2 |dO_i|^2            + |dV|^2)
+    |err dK|^2 = R^2 (scale^2 sum_ij dS_ij^2 |q_i|^2    + |dK|^2)
+    |err dQ|^2 = R^2 (scale^2 sum_ij dS_ij^2 |k_j|^2    + |dQ|^2)
+where the first-pass kernel rounds P (dP - c) and P in place of dS, c near Delta:
+P^2 ((dP - c)^2 + (c - Delta)^2) <= P^2 (2 (dP - Delta)^2 + 3 (c - Delta)^2), and
+c, from 16 keys, is no further from Delta than one key's dP is in the mean.  So
+dQ is held to sqrt(5) times its sum over the keys, and all three to 1.5 of the
+total, as thousands of roundings add up to their mean square.
+
+fp32: a sum of n products is off by sqrt(n) u of its terms' absolute sum, u =
+2^-24 (roundings of independent signs), which carries through the formula
+element by element; the norm of that."""
+
+import math
+
+import pytest
+import torch
+
+import block_testlib as bt
+from test_gpu_cross_attn import make, run
+
+pytestmark = pytest.mark.gpu
+
+R = 2.0**-8 * math.sqrt(0.75 / (2 * math.log(2)) / 3)
+
+
+def parts(x, kv_len, mask):
+    """P, dP, Delta, and what the bounds take of the inputs, in 64 bits, keys of
+    shared heads repeated."""
+    q, k, v, do = (x[n].double() for n in ("q", "k", "v", "do"))
+    B, H, N, D = q.shape
+    G = H // k.shape[1]
+    ok = bt.seen(B, k.shape[2], kv_len, mask, q.device)[:, None, :, None]
+    k, v = (torch.where(ok, t, 0.0).repeat_interleave(G, 1) for t in (k, v))
+    s = (q @ k.mT / math.sqrt(D)).masked_fill(~ok.mT, -math.inf)
+    lse = s.logsumexp(-1, keepdim=True)
+    p = (s - lse.masked_fill(lse == -math.inf, 0.0)).exp()
+    dp = do @ v.mT
+    delta = (p * dp).sum(-1, keepdim=True)
+    return q, k, v, do, s.masked_fill(s == -math.inf, 0.0), p, dp, delta, G
+
+
+def expected(x, want, kv_len, mask):
+    """Norms of the errors of dq, dk and dv."""
+    q, k, v, do, s, p, dp, delta, G = parts(x, kv_len, mask)
+    D, S = q.shape[-1], k.shape[-2]
+    scale = 1.0 / math.sqrt(D)
+    ds = p * (dp - delta)
+    if x["q"].dtype == torch.bfloat16:
+        sq = (lambda t: (t * t).sum(-1))
+        sums = {"dq": 5 * scale**2 * ((ds * ds) @ sq(k)[..., None]).sum(),
+                "dk": scale**2 * ((ds * ds).mT @ sq(q)[..., None]).sum(),
+                "dv": ((p * p).mT @ sq(do)[..., None]).sum()}
+        return {n: 1.5 * R * float(t + sq(want[n][0]).sum()) ** 0.5 for n, t in sums.items()}
+    u, rows = bt.U, q.shape[2] * G
+    e_s = u * (math.sqrt(D) * scale * (q.abs() @ k.abs().mT) + 4 * s.abs() + 4)
+    rel = e_s + (p * e_s).sum(-1, keepdim=True) + u * (math.sqrt(S) + 4)  # of P: its score, lse
+    e_dp = u * math.sqrt(D) * (do.abs() @ v.abs().mT)
+    o = p @ v
+    e_o = (p * (rel + u * math.sqrt(S))) @ v.abs() + u * o.abs()
+    e_delta = (do.abs() * e_o).sum(-1, keepdim=True) + u * math.sqrt(D) * (do * o).abs().sum(-1, keepdim=True)
+    e_ds = rel * ds.abs() + p * (e_dp + e_delta + 2 * u * (dp.abs() + delta.abs()))
+    group = (lambda t: t.unflatten(1, (-1, G)).sum(2))
+    out = {"dq": scale * ((e_ds + u * math.sqrt(S) * ds.abs()) @ k.abs()),
+           "dk": scale * group((e_ds + u * math.sqrt(rows) * ds.abs()).mT @ q.abs()),
+           "dv": group((p * (rel + u * math.sqrt(rows))).mT @ do.abs())}
+    return {n: float((t + u * want[n][0].abs()).norm()) for n, t in out.items()}
+
+
+def hold(x, kv_len=None, mask=None):
+    out = run(x, kv_len, mask)
+    want = bt.cross(x["q"], x["k"], x["v"], kv_len, mask, do=x["do"], bf16=x["q"].dtype == torch.bfloat16)
+    most = expected(x, want, kv_len, mask)
+    far = {n: float((out[n].double() - want[n][0]).norm()) / most[n] for n in most}
+    assert max(far.values()) <= 1, far
+
+
+SHAPES = [
+    # B, H, Hkv, N, S, D
+    (2, 4, 2, 127, 128, 128),
+    (1, 2, 1, 300, 333, 128),
+    (2, 2, 2, 200, 256, 64),
+    (3, 8, 2, 97, 512, 64),
+    (1, 16, 4, 17, 2500, 128),
+    (1, 2, 2, 2500, 80, 64),
+    (1, 2, 2, 1111, 700, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_norms(shape, dtype):
+    hold(make(*shape, dtype, seed=51))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_norms_masked(shape, dtype):
+    B, _, _, _, S, _ = shape
+    g = torch.Generator(device="cuda").manual_seed(52)
+    lens = torch.tensor([S, S - S // 3, S // 2][:B], dtype=torch.int32, device="cuda")
+    hold(make(*shape, dtype, seed=53), lens, (torch.rand(B, S, generator=g, device="cuda") < 0.8).to(torch.uint8))
