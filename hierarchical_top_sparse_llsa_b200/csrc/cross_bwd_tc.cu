@@ -16,9 +16,9 @@
 // number c per row, dS = P (dP - c) + P (c - Delta), so
 //   dQ = scale (sum_j P (dP - c) K + (c - Delta) sum_j P K),
 //   Delta = c sum_j P + sum_j P (dP - c);
-// c is what the item's first 16 keys tell of Delta: their part of the sum, and
-// their mean for the probability that the other keys have.  It takes off what
-// the values have in common, so the rounding of P (dP - c) to bf16 is about
+// c is what 16 of the item's keys tell of Delta, the first 16 with one that is
+// seen: their part of the sum, and their mean for the probability that the other
+// keys have.  It takes off what the values have in common, so the rounding of P (dP - c) to bf16 is about
 // that of dS, and all of it is exact in c.  (Delta from the stored O would carry
 // O's rounding to bf16, which the keys' common part lifts above the gradient
 // where many keys share a row: dQ was up to 7.2e-3 off.)
@@ -218,6 +218,26 @@ struct BwdItems {
     return m >= 64 ? 4 : (m + 15) >> 4;
   }
 };
+
+// Of key tiles n0 .. n0 + n - 1 of entry b, the place of the first with a key
+// that is seen, 0 where none has one (a whole warp asks).
+__device__ __forceinline__ int first_seen(const CrossParams& p, int b, int len, int n0, int n) {
+  if (p.mask == nullptr) return 0;
+  const uint8_t* m = p.mask + (size_t)b * p.S;
+  const int lane = threadIdx.x & 31, end = min(len, (n0 + n) * 64);
+  for (int k0 = n0 * 64; k0 < end; k0 += 256) {
+    bool on[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + 32 * u + lane;
+      on[u] = k < end && m[k] != 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (__any_sync(0xffffffffu, on[u])) return (k0 >> 6) + (u >> 1) - n0;
+  }
+  return 0;
+}
 
 // -lse in units of log2; without keys (lse = -inf) every probability is zero.
 __device__ __forceinline__ float neg_lse2(float lse) { return lse == -INFINITY ? lse : -lse * kLog2e; }
@@ -659,6 +679,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     uint32_t turn = 0;    // parity of its stage
     int j = g;            // its next tile of the item
     Ring<C::kSums> rx;
+    int of_b = -1, of_split = -1, c_tile = 0;  // first pass: the item's tile that c is taken from
     float lse_next = 0.f;
     if (kDq) lse_next = p.lse_in[it.peek(r)];
     for (; ok && it.next();) {
@@ -668,13 +689,18 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         if (it.n == 0) continue;
         const float nl = it.r0 + r < p.N ? neg_lse2(lse) : -INFINITY;  // rows past the end: probability zero
         const uint64_t nl2 = f2_make(nl, nl);
+        if (clean && (it.b != of_b || it.split != of_split)) {
+          of_b = it.b;
+          of_split = it.split;
+          c_tile = first_seen(p, it.b, it.len, it.n0, it.n);
+        }
         bool have_c = false;
         uint64_t c2 = 0, ls = 0, ds = 0;
         for (; j < it.n; j += NG, rn.next(NG), turn ^= 1u) {
           // S first: it tells that the rounds before of the other two are over,
           // which this group may not have seen
           if (!wait(s_full + 8 * g, turn)) break;
-          const bool other = !have_c && j > 0;  // another group has the item's first tile
+          const bool other = !have_c && j > c_tile;  // another group has the tile of c
           const bool x_seen = !clean || look(rn.at(n_aux), rn.parity), c_seen = !other || look(rx.at(c_full), rx.parity);
           if (!finish(x_seen, rn.at(n_aux), rn.parity) || !finish(c_seen, rx.at(c_full), rx.parity)) break;
           if (other) {
@@ -694,14 +720,26 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
               hide16(ts + 64 + 16 * c, bits, 0.f);
             }
           }
-          if (!have_c) {
+          if (j == c_tile) {  // the tiles before see nothing: their P and dP are zero
+            uint32_t bits = 0xffffu, at = 0;  // of the first 16 keys with one that is seen
+            if (clean) {
+              bits = S.bits[rn.i][0];
+              if (bits == 0u && S.bits[rn.i][1] != 0u) {
+                bits = S.bits[rn.i][1];
+                at = 32;
+              }
+              if ((bits & 0xffffu) == 0u && bits != 0u) {
+                bits >>= 16;
+                at += 16;
+              }
+              bits &= 0xffffu;
+            } else if (left < 16) {
+              bits = (1u << left) - 1u;
+            }
             float x[16], d[16];
-            tmem_ld16(ts, x);
-            tmem_ld16(ts + 64, d);
+            tmem_ld16(ts + at, x);
+            tmem_ld16(ts + 64 + at, d);
             tmem_wait_ld();
-            uint32_t bits = 0xffffu;
-            if (clean) bits = S.bits[rn.i][0] & 0xffffu;
-            else if (left < 16) bits = (1u << left) - 1u;
             float w = 0.f, wd = 0.f, t = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {

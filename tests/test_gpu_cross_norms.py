@@ -111,3 +111,23 @@ def test_norms_masked(shape, dtype):
     g = torch.Generator(device="cuda").manual_seed(52)
     lens = torch.tensor([S, S - S // 3, S // 2][:B], dtype=torch.int32, device="cuda")
     hold(make(*shape, dtype, seed=53), lens, (torch.rand(B, S, generator=g, device="cuda") < 0.8).to(torch.uint8))
+
+
+@pytest.mark.parametrize("front", [0, 7, 16, 40, 64, 130])
+@pytest.mark.parametrize("shape", [(2, 4, 2, 300, 333, 64), (1, 2, 2, 200, 300, 128), (1, 4, 1, 9, 3000, 64),
+                                   (2, 8, 8, 1300, 200, 64), (2, 6, 6, 1700, 300, 128)], ids=str)
+def test_common_part_behind_hidden_keys(shape, front):
+    """Keys and values with a large common part, the front of the sequence
+    hidden (a caption padded on the left): what the values share must leave dQ
+    wherever the first key that is seen lies, with the keys in one piece (the
+    last two shapes) and split."""
+    B, _, _, _, S, _ = shape
+    x = make(*shape, "bf16", seed=54, gain=0.3)
+    for n in "kv":
+        x[n] = (x[n].float() + 16.0).to(torch.bfloat16)
+    mask = torch.ones(B, S, dtype=torch.uint8, device="cuda")
+    mask[:, :front] = 0
+    if B > 1:
+        mask[1, S // 2 :] = 0  # and unlike fronts
+        mask[1, : front // 2 + 3] = 0
+    hold(x, None, mask)
