@@ -52,7 +52,9 @@ RopeFreqs rope_freqs(const llsa_rope_desc* r) {
   if (r->scaling == LLSA_ROPE_SCALE_YARN) {
     const double fast = r->beta_fast != 0.0 ? r->beta_fast : 32.0, slow = r->beta_slow != 0.0 ? r->beta_slow : 1.0;
     lo = fmax(floor(n * log((double)r->orig_len / (fast * kTwoPi)) / log(base)), 0.0);
-    hi = fmin(ceil(n * log((double)r->orig_len / (slow * kTwoPi)) / log(base)), n - 1.0);
+    // up to the axis's channels less one, not its pairs: where even the slowest
+    // pair turns within orig_len the ramp's end lies past the last pair
+    hi = fmin(ceil(n * log((double)r->orig_len / (slow * kTwoPi)) / log(base)), 2.0 * n - 1.0);
   }
   for (int j = 0; j < f.n; ++j) {
     double w = pow(base, -(double)j / n);

@@ -378,7 +378,7 @@ LLSA_API int llsa_reorder(int B, int H, int img_h, int img_w, int D, int dtype, 
  *   LLSA_ROPE_SCALE_YARN     f_j / factor * r_j + f_j * (1 - r_j), with
  *                            r_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1),
  *                            lo = max(floor(x(beta_fast)), 0),
- *                            hi = min(ceil(x(beta_slow)), n - 1),
+ *                            hi = min(ceil(x(beta_slow)), 2 n - 1),
  *                            x(beta) = n ln(orig_len / (2 pi beta)) / ln(base)
  */
 enum { LLSA_ROPE_HALF = 0, LLSA_ROPE_INTERLEAVED = 1 };

@@ -1,0 +1,51 @@
+"""The rotary table on the GPU where its frequencies and angles are hardest."""
+
+import math
+
+import pytest
+import torch
+
+import hierarchical_top_sparse_llsa_b200 as llsa
+
+pytestmark = pytest.mark.gpu
+
+
+def table(rope, rows, half, pos=None):
+    t = torch.full((rows, half, 2), float("nan"), device="cuda")
+    llsa.llsa_rope_table(rope, rows, None if pos is None else pos.data_ptr(), t.data_ptr(),
+                         torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    return t.cpu().double()
+
+
+def yarn(dim, base, factor, orig_len, fast=32.0, slow=1.0):
+    """YaRN's frequencies of an axis of `dim` rotated channels, as its authors
+    compute them: the ends of the ramp by channels, the upper one within dim - 1."""
+    def at(turns):
+        return dim * math.log(orig_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+    low, high = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), dim - 1)
+    out = []
+    for i in range(dim // 2):
+        f = base ** (-2 * i / dim)
+        keep = 1 - min(max((i - low) / max(high - low, 0.001), 0), 1)
+        out.append(f / factor * (1 - keep) + f * keep)
+    return out
+
+
+@pytest.mark.parametrize("rot,axes,base,factor,orig_len", [
+    (128, 1, 10000.0, 4.0, 131072),   # the ramp ends past the last pair
+    (128, 1, 10000.0, 4.0, 8192),     # and before it
+    (16, 2, 10000.0, 4.0, 8192),      # four pairs an axis
+    (64, 1, 1000.0, 16.0, 1 << 24),   # every pair keeps its frequency
+    (2, 1, 10000.0, 2.0, 4096),
+])
+def test_yarn_frequencies(rot, axes, base, factor, orig_len):
+    rope = llsa.make_rope(rot, axes=axes, base=base, scaling=llsa.ROPE_SCALE_YARN, factor=factor, orig_len=orig_len)
+    pos = torch.tensor([0, 1, 2, 3, 1000, 100003], dtype=torch.int32)
+    f = torch.tensor(yarn(rot // axes, base, factor, orig_len) * axes, dtype=torch.float64)
+    got = table(rope, len(pos), rot // 2, pos[:, None].repeat(1, axes).contiguous().cuda())
+    ang = pos.double()[:, None] * f
+    m = 0.1 * math.log(factor) + 1
+    want = torch.stack([ang.cos(), ang.sin()], -1) * m
+    # 2^-22 m of the table, and these angles in 64 bits: 4 roundings of up to 1e5
+    assert float((got - want).abs().max()) <= m * (2.0**-22 + 4 * 2.0**-53 * 100003)
