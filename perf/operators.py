@@ -311,6 +311,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _beta_slow(c, base):
+    """The turns at which the library's YaRN ramp ends where the plain form's
+    does: at the last pair, if one turn (0: the default) lies past it."""
+    if c["scaling"] != _YARN:
+        return 0.0
+    n = c["rot"] // 2 // c["axes"]
+    past = n * math.log(c["orig_len"] / (2 * math.pi)) / math.log(base) > n - 1
+    return c["orig_len"] / (2 * math.pi) * base ** (-(n - 1) / n) * (1 + 1e-9) if past else 0.0
+
+
 def _plan(s):
     """The descriptors, buffers and workspaces that a program keeps."""
     import hierarchical_top_sparse_llsa_b200 as llsa
@@ -319,7 +329,7 @@ def _plan(s):
     p = {"llsa": llsa}
     if c["op"] == "table":
         p["rope"] = llsa.make_rope(c["rot"], axes=c["axes"], base=s["base"], scaling=c["scaling"], factor=c["factor"],
-                                   orig_len=c["orig_len"])
+                                   orig_len=c["orig_len"], beta_slow=_beta_slow(c, s["base"]))
         return p
     dtype = llsa.BF16 if c["dtype"] == "bf16" else llsa.F32
     if c["op"] in ("rope", "rope_pool"):
