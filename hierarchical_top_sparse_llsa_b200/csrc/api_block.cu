@@ -38,7 +38,8 @@ int check_rope(const llsa_rope_desc* r) {
 
 // The frequencies of a checked descriptor, in turns per position.
 RopeFreqs rope_freqs(const llsa_rope_desc* r) {
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  constexpr long double kTwoPiL = 6.283185307179586476925286766559006L;
+  constexpr double kTwoPi = (double)kTwoPiL;
   RopeFreqs f;
   memset(&f, 0, sizeof(f));
   f.half = r->rot_dim / 2;
@@ -46,8 +47,9 @@ RopeFreqs rope_freqs(const llsa_rope_desc* r) {
   f.n = f.half / f.axes;
   const double n = (double)f.n;
   const double factor = r->factor != 0.0 ? r->factor : 1.0;
-  double base = r->base != 0.0 ? r->base : 10000.0;
-  if (r->scaling == LLSA_ROPE_SCALE_NTK && f.n > 1) base *= pow(factor, n / (n - 1.0));
+  const double base = r->base != 0.0 ? r->base : 10000.0;
+  long double wide = base;  // the powers in the long double that this host has
+  if (r->scaling == LLSA_ROPE_SCALE_NTK && f.n > 1) wide *= powl(factor, (long double)f.n / (f.n - 1));
   double lo = 0.0, hi = 0.0;
   if (r->scaling == LLSA_ROPE_SCALE_YARN) {
     const double fast = r->beta_fast != 0.0 ? r->beta_fast : 32.0, slow = r->beta_slow != 0.0 ? r->beta_slow : 1.0;
@@ -57,13 +59,15 @@ RopeFreqs rope_freqs(const llsa_rope_desc* r) {
     hi = fmin(ceil(n * log((double)r->orig_len / (slow * kTwoPi)) / log(base)), 2.0 * n - 1.0);
   }
   for (int j = 0; j < f.n; ++j) {
-    double w = pow(base, -(double)j / n);
+    long double w = powl(wide, -(long double)j / f.n);
     if (r->scaling == LLSA_ROPE_SCALE_LINEAR) w /= factor;
     if (r->scaling == LLSA_ROPE_SCALE_YARN) {
       const double ramp = fmin(fmax(((double)j - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
       w = w / factor * ramp + w * (1.0 - ramp);
     }
-    f.turns[j] = w / kTwoPi;
+    w /= kTwoPiL;
+    f.turns[j].x = (double)w;
+    f.turns[j].y = (double)(w - f.turns[j].x);
   }
   f.m = r->mscale > 0.f ? r->mscale
                         : (r->scaling == LLSA_ROPE_SCALE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f);

@@ -36,15 +36,16 @@ __device__ __forceinline__ uint32_t even_bits(uint32_t v) {
   return v;
 }
 
-// Cosine and sine, times m, of position x at `turns` turns a position.  The
-// angle is held in turns: position * (f / 2 pi) in fp64, its whole turns taken
-// off exactly (x - rint(x) is exact), and only the remainder in [-1/2, 1/2] is
-// rounded to fp32 (sincospi of twice it), so the angle's error is 2^-53 of the
-// turns made plus 2^-24 of a half turn at any position.
-__device__ __forceinline__ float2 turn_of(int x, double turns, float m) {
-  const double t = (double)x * turns;
+// Cosine and sine, times m, of position x at turns.x + turns.y turns a position.
+// The angle is held in turns: its whole turns come off the exact product in one
+// fp64 step, the frequency's rest is added, and only the remainder in [-1/2, 1/2]
+// is rounded to fp32 (sincospi of twice it), so the angle's error is 2^-24 of a
+// half turn at any position.  (Whole turns off the rounded product, without the
+// rest: 2^-22 more near 2^31, and no faster.)
+__device__ __forceinline__ float2 turn_of(int x, double2 turns, float m) {
+  const double p = (double)x;
   float s, c;
-  sincospif(2.0f * (float)(t - rint(t)), &s, &c);
+  sincospif(2.0f * (float)fma(p, turns.y, fma(p, turns.x, -rint(p * turns.x))), &s, &c);
   return make_float2(c * m, s * m);
 }
 
@@ -62,13 +63,18 @@ __device__ __forceinline__ void store_turns(float* row, int half, int p0, float2
 // Thread (r, j): pairs 2 j and 2 j + 1 of rows r, r + step, ...
 __global__ void __launch_bounds__(kTableThreads)
 rope_table_kernel(RopeFreqs f, int rows, const int32_t* __restrict__ pos, float* __restrict__ table) {
+  // Lanes of unlike frequencies take the parameters' constant bank one after the
+  // other, so each is read from there once a CTA.
+  __shared__ double2 turns[kMaxRopeFreqs];
+  if (threadIdx.x < f.n) turns[threadIdx.x] = f.turns[threadIdx.x];
+  __syncthreads();
   const int hp = (f.half + 1) / 2;  // threads per row
   const int per = kTableThreads / hp;
   const int r0 = threadIdx.x / hp, j = threadIdx.x % hp;
   if (r0 >= per) return;
   const int p0 = 2 * j, p1 = min(2 * j + 1, f.half - 1);
   const int a0 = p0 / f.n, a1 = p1 / f.n;
-  const double f0 = f.turns[p0 % f.n], f1 = f.turns[p1 % f.n];
+  const double2 f0 = turns[p0 % f.n], f1 = turns[p1 % f.n];
   for (long long r = (long long)blockIdx.x * per + r0; r < rows; r += (long long)gridDim.x * per) {
     int x0, x1;
     if (pos != nullptr) {
@@ -88,17 +94,17 @@ rope_table_kernel(RopeFreqs f, int rows, const int32_t* __restrict__ pos, float*
 // 16 x 16 pixels, so a CTA forms the turns of its 16 + 16 coordinates and
 // writes each 16 times.  Chosen where more than half of the SMs have a square: its coordinates
 // come before its first store, which only other CTAs can cover.  Computing every
-// entry against this, us: rot_dim 64, 256 rows 3.0 and 5.2, 16384 rows 5.5 and
-// 5.6, 65536 rows 9.9 and 7.1; rot_dim 128, 3.5 and 8.6, 8.6 and 8.8, 14.7 and
-// 12.6.
+// entry against this, us a launch, back to back: rot_dim 64, 256 rows 1.7 and 3.6,
+// 16384 rows 3.5 and 3.7, 65536 rows 8.3 and 5.3; rot_dim 128, 2.1 and 6.2, 6.2
+// and 6.4, 13.1 and 9.5.
 constexpr int kSquare = 256;
 __global__ void __launch_bounds__(kTableThreads)
 rope_table_square_kernel(RopeFreqs f, int rows, float* __restrict__ table) {
-  __shared__ float2 turns[2][16][kMaxRopeFreqs / 2];  // axis, coordinate, frequency
+  __shared__ float2 turns[2][16][kMaxRopeFreqs / 2 + 1];  // axis, coordinate, frequency
   const int r0 = blockIdx.x * kSquare;
   const int x0 = (int)even_bits((uint32_t)r0), y0 = (int)even_bits((uint32_t)r0 >> 1);
   for (int i = threadIdx.x; i < 32 * f.n; i += kTableThreads) {
-    const int k = i / f.n, w = i - k * f.n;
+    const int k = i & 31, w = i >> 5;  // a warp has one frequency
     turns[k >> 4][k & 15][w] = turn_of((k < 16 ? x0 : y0) + (k & 15), f.turns[w], f.m);
   }
   __syncthreads();

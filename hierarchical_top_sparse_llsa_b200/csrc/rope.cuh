@@ -7,9 +7,10 @@ namespace llsa {
 
 constexpr int kMaxRopeFreqs = 64;  // rot_dim / 2 <= 64
 
-// the table's frequencies in turns per position, f_j / 2 pi, j < n
+// the table's frequencies in turns per position, f_j / 2 pi, j < n, each the sum
+// of two doubles: far positions multiply what one leaves off
 struct RopeFreqs {
-  double turns[kMaxRopeFreqs];
+  double2 turns[kMaxRopeFreqs];
   int half;   // pairs per row, rot_dim / 2
   int n;      // pairs per axis
   int axes;

@@ -407,7 +407,7 @@ typedef struct {
  * llsa_rope_table - the cosines and sines that llsa_rope and llsa_rope_pool
  * read.  A program builds it once for its positions and keeps it.
  *   table: fp32 [rows, rot_dim / 2, 2] (cosine, sine of each pair), 16-byte
- *   aligned, written.  Angles are formed and reduced in fp64, so positions
+ *   aligned, written.  Angles are formed and reduced in more than fp64, so positions
  *   far into a context lose nothing; each entry is within 2^-22 m of the
  *   exact value.
  *   pos: int32 [rows, axes], any values, or NULL: row r is token r, whose

@@ -1,6 +1,7 @@
 """The rotary table on the GPU where its frequencies and angles are hardest."""
 
 import math
+from decimal import Decimal, getcontext
 
 import pytest
 import torch
@@ -49,3 +50,36 @@ def test_yarn_frequencies(rot, axes, base, factor, orig_len):
     want = torch.stack([ang.cos(), ang.sin()], -1) * m
     # 2^-22 m of the table, and these angles in 64 bits: 4 roundings of up to 1e5
     assert float((got - want).abs().max()) <= m * (2.0**-22 + 4 * 2.0**-53 * 100003)
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+
+
+@pytest.mark.parametrize("rot,base,kw", [
+    (128, 10000.0, {}),
+    (64, 500000.0, {}),
+    (64, 10500.0, dict(scaling=llsa.ROPE_SCALE_LINEAR, factor=3.0)),
+    (64, 10000.0, dict(scaling=llsa.ROPE_SCALE_NTK, factor=8.0)),
+    (2, 10000.0, dict(mscale=1.75)),
+])
+def test_table_as_far_as_positions_go(rot, base, kw):
+    """Each entry is within 2^-22 m of the exact value at any int32 position,
+    against angles of 50 digits."""
+    getcontext().prec = 50
+    n, factor = rot // 2, Decimal(kw.get("factor", 1.0))
+    b = Decimal(base)
+    if kw.get("scaling") == llsa.ROPE_SCALE_NTK:
+        b *= factor ** (Decimal(n) / (n - 1))
+    f = [b ** (-Decimal(j) / n) for j in range(n)]
+    if kw.get("scaling") == llsa.ROPE_SCALE_LINEAR:
+        f = [w / factor for w in f]
+    pos = torch.randint(2**31 - 4096, 2**31, (40,), generator=torch.Generator().manual_seed(3), dtype=torch.int64)
+    pos = torch.cat([pos, -pos, torch.tensor([-(2**31), 2**31 - 1, 0, 1 << 24, 1 << 28, 123456789])])
+    got = table(llsa.make_rope(rot, base=base, **kw), len(pos), n, pos.to(torch.int32).cuda())
+    want = torch.empty(len(pos), n, 2, dtype=torch.float64)
+    for i, p in enumerate(pos.tolist()):
+        for j, w in enumerate(f):
+            ang = float((p * w) % (2 * PI))  # rounded to 64 bits once reduced
+            want[i, j, 0], want[i, j, 1] = math.cos(ang), math.sin(ang)
+    m = kw.get("mscale", 1.0)
+    assert float((got - want * m).abs().max()) <= m * 2.0**-22
