@@ -180,8 +180,10 @@ CrossWs cross_bwd_ws(const llsa_cross_desc* d) {
   const size_t rows = (size_t)d->B * d->H * d->N;
   // keys, in whole tiles where the parts are
   const size_t keys = (size_t)BH * (tc ? ((size_t)d->S + 127) / 128 * 128 : (size_t)d->S);
-  w.delta = take(&w.total, rows * sizeof(float));
-  w.alone = take(&w.total, (size_t)d->B * sizeof(int32_t));
+  if (tc) {  // what the first pass leaves the second
+    w.delta = take(&w.total, rows * sizeof(float));
+    w.alone = take(&w.total, (size_t)d->B * sizeof(int32_t));
+  }
   if (w.plan.nks > 1) {
     w.a = take(&w.total, w.plan.nks * rows * d->D * sizeof(float));
     if (tc) {
@@ -452,8 +454,10 @@ int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* 
   p.dk = dk;
   p.dv = dv;
   char* base = static_cast<char*>(ws);
-  p.delta = reinterpret_cast<float*>(base + w.delta);
-  p.alone = reinterpret_cast<int32_t*>(base + w.alone);
+  if (desc->dtype == LLSA_BF16) {
+    p.delta = reinterpret_cast<float*>(base + w.delta);
+    p.alone = reinterpret_cast<int32_t*>(base + w.alone);
+  }
   if (p.nks > 1) {
     p.part_dq = reinterpret_cast<float*>(base + w.a);
     p.part_dqb = reinterpret_cast<float*>(base + w.a2);

@@ -36,13 +36,13 @@ struct CrossParams {
   void* dv;
   float* part_o;   // fwd, nks > 1: [nks][B H N][D], the splits' unnormalised O
   float2* part_ml; // fwd, nks > 1: [nks][B H N], their maxima (base 2) and sums
-  float* delta;    // bwd: [B H N]
+  float* delta;    // bwd of bf16: [B H N]
   float* part_dq;  // bwd, nks > 1: [nks][B H N][D]
   float* part_dqb; // bwd of bf16, nks > 1: the same again, and
   float4* part_s;  // [nks][B H N]: c, sum P, sum P (dP - c), whether the parts are written
   float* part_dk;  // bwd, nz > 1: [nz][B H S][D]; of bf16 [B H key tiles of 128][nz][128][D]
   float* part_dv;
-  int32_t* alone;  // bwd: [B], whether the entry sees at most one key
+  int32_t* alone;  // bwd of bf16: [B], whether the entry sees at most one key
   int32_t* status;
   // The query heads of a key head are neighbours in memory and see the same
   // keys: the kernels take them as one run of rows.

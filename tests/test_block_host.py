@@ -270,3 +270,11 @@ def test_frequency_scalings():
     yarn = bt.inv_freq(32, scaling=3, factor=4.0, orig_len=2048)
     assert yarn[0] == plain[0] and math.isclose(yarn[-1], plain[-1] / 4, rel_tol=1e-12)
     assert ((yarn <= plain) & (yarn >= plain / 4 * (1 - 1e-12))).all()
+
+
+def test_cross_fp32_backward_without_parts_needs_no_workspace():
+    # as many tiles as SMs several times over: nothing is cut
+    d = desc(B=8, H=16, Hkv=16, N=1024, S=77, dtype=llsa.F32)
+    assert llsa.llsa_cross_bwd_workspace_bytes(d) == 0
+    d.dtype = llsa.BF16  # Delta and a number per entry
+    assert llsa.llsa_cross_bwd_workspace_bytes(d) >= 8 * 16 * 1024 * 4

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import block_testlib as bt
+import hierarchical_top_sparse_llsa_b200 as llsa
 from test_gpu_cross_attn import make, run
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,22 @@ def test_items_without_rows_for_every_tile(S, N, masked):
     for _ in range(3):
         b = run(x, lens, mask, grads=False)
         assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_fp32_backward_without_a_workspace():
+    shape = (8, 16, 16, 1024, 77, 64)
+    x = make(*shape, "f32", seed=46)
+    B, H, Hkv, N, S, D = shape
+    d = llsa.make_cross(B, H, Hkv, N, S, D, llsa.F32)
+    assert llsa.llsa_cross_fwd_workspace_bytes(d) == 0 and llsa.llsa_cross_bwd_workspace_bytes(d) == 0
+    o, lse = torch.empty_like(x["q"]), torch.empty(B, H, N, device="cuda")
+    g = {n: torch.empty_like(x[n]) for n in "qkv"}
+    q, k, v, do = (x[n].data_ptr() for n in ("q", "k", "v", "do"))
+    s = torch.cuda.current_stream().cuda_stream
+    llsa.llsa_cross_attn_fwd(d, q, k, v, None, None, o.data_ptr(), None, lse.data_ptr(), None, 0, None, s)
+    llsa.llsa_cross_attn_bwd(d, q, k, v, None, None, o.data_ptr(), None, lse.data_ptr(), do, g["q"].data_ptr(),
+                             g["k"].data_ptr(), g["v"].data_ptr(), None, 0, None, s)
+    torch.cuda.synchronize()
+    want = bt.cross(x["q"], x["k"], x["v"], do=x["do"], bf16=False)
+    for n, t in (("o", o), ("lse", lse), ("dq", g["q"]), ("dk", g["k"]), ("dv", g["v"])):
+        bt.within(t, *want[n], n)
