@@ -305,7 +305,6 @@ cudaError_t launch_rope_typed(RopeParams p, cudaStream_t s) {
   const long long want = 8LL * kSms;
   long long parts = (want + blocks - 1) / blocks;
   if (parts > rows) parts = rows;
-  if (parts < (rows + 65534) / 65535) parts = (rows + 65534) / 65535;
   p.per = (int)((rows + parts - 1) / parts);
   const dim3 grid((unsigned)blocks, (unsigned)((rows + p.per - 1) / p.per));
   if (ragged) rope_ragged_kernel<T><<<grid, kRopeThreads, 0, s>>>(p);

@@ -6,6 +6,7 @@ from decimal import Decimal, getcontext
 import pytest
 import torch
 
+import block_testlib as bt
 import hierarchical_top_sparse_llsa_b200 as llsa
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +84,23 @@ def test_table_as_far_as_positions_go(rot, base, kw):
             want[i, j, 0], want[i, j, 1] = math.cos(ang), math.sin(ang)
     m = kw.get("mscale", 1.0)
     assert float((got - want * m).abs().max()) <= m * 2.0**-22
+
+
+@pytest.mark.parametrize("k", [True, False])
+def test_more_heads_than_a_grid_has_rows(k):
+    """100000 heads of one token: a thread walks many of them."""
+    H, D = 100000, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = [torch.randn(1, H, 1, D, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    rope = llsa.make_rope(D)
+    tab = torch.empty(1, D // 2, 2, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    pos = torch.tensor([[1234]], dtype=torch.int32, device="cuda")
+    llsa.llsa_rope_table(rope, 1, pos.data_ptr(), tab.data_ptr(), s)
+    out = [torch.full_like(t, float("nan")) for t in x]
+    llsa.llsa_rope(rope, 1, H, 1, D, llsa.BF16, tab.data_ptr(), 1, x[0].data_ptr(), x[1].data_ptr() if k else None,
+                   out[0].data_ptr(), out[1].data_ptr() if k else None, False, s)
+    torch.cuda.synchronize()
+    for t, y in zip(x[: 1 + k], out):
+        want, mag = bt.rotate(t.double(), tab.double(), D, False)
+        bt.within(y, want, bt.rotate_bound(want, mag, True), "rotation")
