@@ -437,6 +437,8 @@ int llsa_cross_attn_bwd(const llsa_cross_desc* desc, const void* q, const void* 
   for (const void* ptr : ptrs)
     if (!aligned(ptr, 16)) return LLSA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(kv_len, 4)) return LLSA_ERR_INVALID_ARG;
+  // the second pass forms lse / sm_scale, which must not pass fp32
+  if (desc->dtype == LLSA_BF16 && desc->sm_scale > 0.f && desc->sm_scale < 0x1p-120f) return LLSA_ERR_UNSUPPORTED;
   const CrossWs w = cross_bwd_ws(desc);
   st = check_ws(ws, ws_bytes, w.total);
   if (st != LLSA_OK) return st;

@@ -510,6 +510,8 @@ LLSA_API int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, con
  *   with the sums over i running over every query head that reads the key
  *   head.  States that are not seen get zero gradients, and so do the scores of
  *   a query that sees one state only (its probability is 1 whatever the score).
+ *   dtype LLSA_BF16: sm_scale is 0 or at least 2^-120 (else
+ *   LLSA_ERR_UNSUPPORTED).
  *   o, lse: the forward's outputs.  dtype LLSA_F32 takes Delta_i = dO_i . o_i;
  *   with LLSA_BF16 o must be valid but is not read, nor is o_res (may be NULL):
  *   Delta is formed from unrounded terms, as O itself is stored rounded.

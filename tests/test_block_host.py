@@ -278,3 +278,11 @@ def test_cross_fp32_backward_without_parts_needs_no_workspace():
     assert llsa.llsa_cross_bwd_workspace_bytes(d) == 0
     d.dtype = llsa.BF16  # Delta and a number per entry
     assert llsa.llsa_cross_bwd_workspace_bytes(d) >= 8 * 16 * 1024 * 4
+
+
+@pytest.mark.parametrize("scale", [2.0**-121, 1e-38, 1e-45])
+def test_cross_bf16_backward_refuses_scales_that_lse_cannot_be_divided_by(scale):
+    d = desc()
+    d.sm_scale = scale
+    assert 0 < d.sm_scale < 2.0**-120
+    assert cross("bwd", d) == llsa.ERR_UNSUPPORTED

@@ -8,7 +8,7 @@ import torch
 
 import block_testlib as bt
 import hierarchical_top_sparse_llsa_b200 as llsa
-from test_gpu_cross_attn import make, run
+from test_gpu_cross_attn import check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +102,11 @@ def test_fp32_backward_without_a_workspace():
     want = bt.cross(x["q"], x["k"], x["v"], do=x["do"], bf16=False)
     for n, t in (("o", o), ("lse", lse), ("dq", g["q"]), ("dk", g["k"]), ("dv", g["v"])):
         bt.within(t, *want[n], n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0**-120, 2.0**-40, 2.0**-10, 4.0])
+def test_smallest_and_large_scales(scale, dtype):
+    shape = (1, 2, 1, 150, 200, 64)
+    x = make(*shape, dtype, seed=47)
+    check(x, run(x, scale=scale), scale=scale)
