@@ -161,6 +161,9 @@ def lib() -> ctypes.CDLL:
             "llsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "llsa_version": (ctypes.c_int, []),
         }
+        missing = [name for name in sig if not hasattr(L, name)]
+        if missing:  # calls are added without a new version, which is that of the struct layouts
+            raise LlsaError(f"{LIB_PATH} lacks {', '.join(missing)}: rebuild the CUDA library")
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
             fn.restype = res

@@ -286,3 +286,14 @@ def test_cross_bf16_backward_refuses_scales_that_lse_cannot_be_divided_by(scale)
     d.sm_scale = scale
     assert 0 < d.sm_scale < 2.0**-120
     assert cross("bwd", d) == llsa.ERR_UNSUPPORTED
+
+
+def test_binding_refuses_a_library_without_its_calls(monkeypatch):
+    """A library built before a call was added has the same version: the
+    binding names what is missing."""
+    import _ctypes  # any shared object that is not this library
+
+    monkeypatch.setattr(llsa, "_lib", None)
+    monkeypatch.setattr(llsa, "LIB_PATH", _ctypes.__file__)
+    with pytest.raises(llsa.LlsaError, match="llsa_cross_attn_bwd.*rebuild"):
+        llsa.lib()
