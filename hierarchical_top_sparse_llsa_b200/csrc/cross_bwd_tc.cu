@@ -16,10 +16,10 @@
 // number c per row, dS = P (dP - c) + P (c - Delta), so
 //   dQ = scale (sum_j P (dP - c) K + (c - Delta) sum_j P K),
 //   Delta = c sum_j P + sum_j P (dP - c);
-// c is what 16 of the item's keys tell of Delta, the first 16 with one that is
-// seen: their part of the sum, and their mean for the probability that the other
-// keys have.  It takes off what the values have in common, so the rounding of P (dP - c) to bf16 is about
-// that of dS, and all of it is exact in c.  (Delta from the stored O would carry
+// c is dO . O with O as the forward stored it, rounded to bf16 on top, which is
+// near Delta in every row.  So the rounding of P (dP - c) to bf16 is that of dS,
+// and all of it is exact in c.  (c from some of the item's keys left dQ off by up
+// to 1.1e-2 where rows sit on other keys, 2.4e-3 now.)  (Delta from the stored O would carry
 // O's rounding to bf16, which the keys' common part lifts above the gradient
 // where many keys share a row: dQ was up to 7.2e-3 off.)
 // A query that sees one key alone has dS = 0: P is 1 whatever the score.
@@ -32,6 +32,7 @@
 //   load    TMA loads of A (two buffers) and N (a ring);
 //   mma     issues S and dP; prod the products.  One warp for both would leave
 //           the tensor cores idle between its waits;
+//   dot     (four) first pass: c;
 //   aux     first pass: with lengths or a mask, the bits of the keys seen and
 //           zeros over the K rows that are not (their dS is zero, and zero
 //           times NaN is NaN); second pass: lse and Delta of the queries that
@@ -66,7 +67,7 @@ struct Sizes {
   // warp sees every round of its slots: a barrier is not waited for before the
   // round before has been seen, which its parity would not tell apart.
   static constexpr int kAuxWarps = 3;
-  static constexpr int kThreads = (kAux + kAuxWarps) * 32;
+  static constexpr int kDot = kAux + kAuxWarps;  // first pass: four warps for c
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
   static constexpr int kSlots = (D == 64) ? 6 : 3;
@@ -78,17 +79,17 @@ template <typename C>
 struct Shared {
   uint64_t a_full[C::kBufs], a_empty[C::kBufs], n_full[C::kSlots], n_empty[C::kSlots], n_aux[C::kSlots];
   uint64_t s_full[C::kStages], p_full[C::kStages], acc_full, acc_free, staged, done;
-  uint64_t c_full[C::kSums], x_full[C::kSums], x_read[C::kSums];
+  uint64_t c_full[2], c_read[2], x_full[C::kSums], x_read[C::kSums];
   uint32_t tmem_base;
   uint32_t bits[C::kSlots][2];  // first pass: keys seen, by slot
   typename C::Side side;
 };
 
-// First pass: of the rows of an item (two of them where there is room).
+// First pass: of the rows of an item (the sums of two of them where there is room).
 template <int kSums, int kStages>
 struct RowSums {
   static constexpr int kHeld = kSums;
-  float c[kSums][128];
+  bf16 c[2][128];
   float2 sums[kSums][kStages][128];  // each group's sum P, sum P (dP - c)
 };
 
@@ -107,6 +108,7 @@ struct ColumnTerms {
 template <int D, bool kDq>
 struct Cfg : Sizes<D> {
   using Z = Sizes<D>;
+  static constexpr int kThreads = (Z::kDot + (kDq ? 4 : 0)) * 32;
   // buffers of A1, A2: the second pass has few items
   static constexpr int kBufs = (D == 64 || kDq) ? 2 : 1;
   static constexpr int kOffN = kBufs * 2 * Z::kA;
@@ -219,25 +221,8 @@ struct BwdItems {
   }
 };
 
-// Of key tiles n0 .. n0 + n - 1 of entry b, the place of the first with a key
-// that is seen, 0 where none has one (a whole warp asks).
-__device__ __forceinline__ int first_seen(const CrossParams& p, int b, int len, int n0, int n) {
-  if (p.mask == nullptr) return 0;
-  const uint8_t* m = p.mask + (size_t)b * p.S;
-  const int lane = threadIdx.x & 31, end = min(len, (n0 + n) * 64);
-  for (int k0 = n0 * 64; k0 < end; k0 += 256) {
-    bool on[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int k = k0 + 32 * u + lane;
-      on[u] = k < end && m[k] != 0;
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (__any_sync(0xffffffffu, on[u])) return (k0 >> 6) + (u >> 1) - n0;
-  }
-  return 0;
-}
+using bf16x2 = __nv_bfloat162;
+__device__ __forceinline__ bf16x2 as_bf16x2(uint32_t x) { return *reinterpret_cast<bf16x2*>(&x); }
 
 // -lse in units of log2; without keys (lse = -inf) every probability is zero.
 __device__ __forceinline__ float neg_lse2(float lse) { return lse == -INFINITY ? lse : -lse * kLog2e; }
@@ -285,8 +270,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     mbar_init(smem_u32(&S.acc_full), 1);
     mbar_init(smem_u32(&S.acc_free), 128);
     mbar_init(smem_u32(&S.staged), 128);
-    for (int i = 0; i < C::kSums; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&S.c_full[i]), 128);
+      mbar_init(smem_u32(&S.c_read[i]), (NG + 1) * 128);
+    }
+    for (int i = 0; i < C::kSums; ++i) {
       mbar_init(smem_u32(&S.x_full[i]), NG * 128);
       mbar_init(smem_u32(&S.x_read[i]), 128);
     }
@@ -307,7 +295,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
   const uint32_t a_full = smem_u32(S.a_full), a_empty = smem_u32(S.a_empty), n_full = smem_u32(S.n_full),
                  n_empty = smem_u32(S.n_empty), n_aux = smem_u32(S.n_aux), s_full = smem_u32(S.s_full),
                  p_full = smem_u32(S.p_full), acc_full = smem_u32(&S.acc_full), acc_free = smem_u32(&S.acc_free),
-                 c_full = smem_u32(S.c_full), x_full = smem_u32(S.x_full), x_read = smem_u32(S.x_read);
+                 c_full = smem_u32(S.c_full), c_read = smem_u32(S.c_read), x_full = smem_u32(S.x_full), x_read = smem_u32(S.x_read);
   // Waits of whole warps.  A look at a barrier takes 150 cycles even where its
   // phase is over: where it can, a warp looks before it does something else
   // (or at two barriers at once) and takes the answer afterwards.
@@ -447,6 +435,56 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     }
     tc_commit_by(lead, smem_u32(&S.done));
     if (!mbar_wait(smem_u32(&S.done), 0)) ok = false;
+  } else if (kDq && warp >= C::kDot) {
+    // c of an item's rows, 32 a warp: L lanes a row, 16 bytes of it each, and L
+    // such steps, whose sums over the lanes then end in one lane each.  A lane
+    // adds its eight products in bf16: any c is right, and this one as near.  dO
+    // is read again rather than taken from its tile, so that c does not wait for
+    // that (336 us against 340 at 256x256 pixels, D = 128 182 against 188).
+    if constexpr (kDq) {
+      constexpr int L = D / 8, kRows = 32 / L;
+      const int first = 32 * (warp - C::kDot) + lane / L, chunk = lane % L;
+      Ring<2> rc;
+      for (; ok && it.next();) {
+        if (it.n == 0) continue;
+        const size_t at = ((size_t)it.bk * p.N + it.r0 + first) * L + chunk;
+        const uint4 *o = static_cast<const uint4*>(p.o_in) + at, *g = static_cast<const uint4*>(p.dout) + at;
+        float s[L];
+#pragma unroll
+        for (int i0 = 0; i0 < L; i0 += 4) {  // eight loads in flight
+          uint4 x[4], y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = y[i] = make_uint4(0, 0, 0, 0);
+            if (it.r0 + first + (i0 + i) * kRows < p.N) {
+              x[i] = __ldg(o + (i0 + i) * 32);
+              y[i] = __ldg(g + (i0 + i) * 32);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, b[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+            bf16x2 t = __hmul2(as_bf16x2(a[0]), as_bf16x2(b[0]));
+#pragma unroll
+            for (int e = 1; e < 4; ++e) t = __hfma2(as_bf16x2(a[e]), as_bf16x2(b[e]), t);
+            s[i0 + i] = __low2float(t) + __high2float(t);
+          }
+        }
+#pragma unroll
+        for (int m = L / 2; m > 0; m /= 2) {
+          const bool up = (chunk & m) != 0;
+#pragma unroll
+          for (int i = 0; i < m; ++i) {
+            const float keep = up ? s[i + m] : s[i], send = up ? s[i] : s[i + m];
+            s[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+          }
+        }
+        if (!wait(rc.at(c_read), rc.parity ^ 1u)) break;
+        S.side.c[rc.i][first + chunk * kRows] = __float2bfloat16_rn(fabsf(s[0]) < 3e38f ? s[0] : 0.f);
+        mbar_arrive(rc.at(c_full));
+        rc.next();
+      }
+    }
   } else if (warp >= C::kAux) {
     constexpr int NA = C::kAuxWarps;
     Ring<NS> rn;
@@ -529,6 +567,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     bool one = false;
     Ring<C::kBufs> ra;
     Ring<C::kSums> rx;
+    Ring<2> rc;
     uint32_t par = 0;  // of acc_full and staged: the item's
     for (; ok && it.next(); ) {
       const int row = it.r0 + r;
@@ -554,8 +593,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           }
           continue;
         }
+        if (!wait(rc.at(c_full), rc.parity)) break;
+        const float c0 = __bfloat162float(S.side.c[rc.i][r]);
+        mbar_arrive(rc.at(c_read));
+        rc.next();
         if (!wait(rx.at(x_full), rx.parity)) break;
-        const float c0 = S.side.c[rx.i][r];
         float sp = 0.f, sd = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -679,7 +721,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     uint32_t turn = 0;    // parity of its stage
     int j = g;            // its next tile of the item
     Ring<C::kSums> rx;
-    int of_b = -1, of_split = -1, c_tile = 0;  // first pass: the item's tile that c is taken from
+    Ring<2> rc;
     float lse_next = 0.f;
     if (kDq) lse_next = p.lse_in[it.peek(r)];
     for (; ok && it.next();) {
@@ -689,25 +731,25 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         if (it.n == 0) continue;
         const float nl = it.r0 + r < p.N ? neg_lse2(lse) : -INFINITY;  // rows past the end: probability zero
         const uint64_t nl2 = f2_make(nl, nl);
-        if (clean && (it.b != of_b || it.split != of_split)) {
-          of_b = it.b;
-          of_split = it.split;
-          c_tile = first_seen(p, it.b, it.len, it.n0, it.n);
-        }
         bool have_c = false;
         uint64_t c2 = 0, ls = 0, ds = 0;
+        const bool c_seen = look(rc.at(c_full), rc.parity);
+        auto take_c = [&]() {
+          have_c = true;
+          if (!finish(c_seen, rc.at(c_full), rc.parity)) return false;
+          const float c0 = __bfloat162float(S.side.c[rc.i][r]);
+          c2 = f2_make(c0, c0);
+          mbar_arrive(rc.at(c_read));
+          rc.next();
+          return true;
+        };
         for (; j < it.n; j += NG, rn.next(NG), turn ^= 1u) {
-          // S first: it tells that the rounds before of the other two are over,
-          // which this group may not have seen
+          // S first: it tells that the round before of n_aux is over, which this
+          // group may not have seen
           if (!wait(s_full + 8 * g, turn)) break;
-          const bool other = !have_c && j > c_tile;  // another group has the tile of c
-          const bool x_seen = !clean || look(rn.at(n_aux), rn.parity), c_seen = !other || look(rx.at(c_full), rx.parity);
-          if (!finish(x_seen, rn.at(n_aux), rn.parity) || !finish(c_seen, rx.at(c_full), rx.parity)) break;
-          if (other) {
-            const float c0 = S.side.c[rx.i][r];
-            c2 = f2_make(c0, c0);
-            have_c = true;
-          }
+          const bool x_seen = !clean || look(rn.at(n_aux), rn.parity);
+          if (!have_c && !take_c()) break;
+          if (!finish(x_seen, rn.at(n_aux), rn.parity)) break;
           tc_fence_after();
           const int nt = it.steps(j), left = it.len - (it.n0 + j) * 64;
           if (clean || left < 64) {
@@ -719,41 +761,6 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
               hide16(ts + 16 * c, bits, -INFINITY);
               hide16(ts + 64 + 16 * c, bits, 0.f);
             }
-          }
-          if (j == c_tile) {  // the tiles before see nothing: their P and dP are zero
-            uint32_t bits = 0xffffu, at = 0;  // of the first 16 keys with one that is seen
-            if (clean) {
-              bits = S.bits[rn.i][0];
-              if (bits == 0u && S.bits[rn.i][1] != 0u) {
-                bits = S.bits[rn.i][1];
-                at = 32;
-              }
-              if ((bits & 0xffffu) == 0u && bits != 0u) {
-                bits >>= 16;
-                at += 16;
-              }
-              bits &= 0xffffu;
-            } else if (left < 16) {
-              bits = (1u << left) - 1u;
-            }
-            float x[16], d[16];
-            tmem_ld16(ts + at, x);
-            tmem_ld16(ts + 64 + at, d);
-            tmem_wait_ld();
-            float w = 0.f, wd = 0.f, t = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float e = ex2_approx(fmaf(x[i], sc2, nl));
-              w += e;
-              wd = fmaf(e, d[i], wd);
-              t += d[i];
-            }
-            const float c0 = fmaf(1.f - w, t / (float)max(1, __popc(bits)), wd);
-            c2 = f2_make(c0, c0);
-            have_c = true;
-            if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
-            S.side.c[rx.i][r] = c0;
-            mbar_arrive(rx.at(c_full));
           }
 #pragma unroll 1
           for (int c = 0; c < nt; ++c) {  // 16 keys
@@ -782,7 +789,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
           tc_fence_before();
           mbar_arrive(p_full + 8 * g);
         }
-        if (!ok) break;
+        if (!ok || (!have_c && !take_c())) break;
         j -= it.n;
         if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
         const float2 l2 = f2_split(ls), d2 = f2_split(ds);

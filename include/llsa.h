@@ -513,8 +513,11 @@ LLSA_API int llsa_cross_attn_fwd(const llsa_cross_desc* desc, const void* q, con
  *   dtype LLSA_BF16: sm_scale is 0 or at least 2^-120 (else
  *   LLSA_ERR_UNSUPPORTED).
  *   o, lse: the forward's outputs.  dtype LLSA_F32 takes Delta_i = dO_i . o_i;
- *   with LLSA_BF16 o must be valid but is not read, nor is o_res (may be NULL):
- *   Delta is formed from unrounded terms, as O itself is stored rounded.
+ *   LLSA_BF16 forms Delta from unrounded terms, as O is stored rounded, and takes
+ *   dO_i . o_i off dO_i . v_j before it rounds their products with P, which keeps
+ *   that rounding small.  o_res is not read (may be NULL).
+ *   With LLSA_BF16, P_ij and dS_ij are rounded to bf16 for the sums over j and i,
+ *   as is P_ij in the forward's, and sums are fp32.
  *   dout: dO.  dq: [B, H, N, D], dk, dv: [B, Hkv, S, D], of dtype, written (dk,
  *   dv may be NULL when S = 0).  All 16-byte aligned.  kv_len, key_mask: as the
  *   forward took them.
