@@ -39,7 +39,7 @@ struct CrossParams {
   float* delta;    // bwd of bf16: [B H N]
   float* part_dq;  // bwd, nks > 1: [nks][B H N][D]
   float* part_dqb; // bwd of bf16, nks > 1: the same again, and
-  float4* part_s;  // [nks][B H N]: c, sum P, sum P (dP - c), whether the parts are written
+  float4* part_s;  // [nks][B H N]: c, sum P (dP - c), the sum of its rounded terms, whether the parts are written
   float* part_dk;  // bwd, nz > 1: [nz][B H S][D]; of bf16 [B H key tiles of 128][nz][128][D]
   float* part_dv;
   int32_t* alone;  // bwd of bf16: [B], whether the entry sees at most one key

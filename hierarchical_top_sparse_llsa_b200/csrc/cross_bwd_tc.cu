@@ -14,14 +14,19 @@
 //
 // Delta is formed from unrounded terms and in the same walk as dQ.  With any
 // number c per row, dS = P (dP - c) + P (c - Delta), so
-//   dQ = scale (sum_j P (dP - c) K + (c - Delta) sum_j P K),
-//   Delta = c sum_j P + sum_j P (dP - c);
-// c is dO . O with O as the forward stored it, rounded to bf16 on top, which is
-// near Delta in every row.  So the rounding of P (dP - c) to bf16 is that of dS,
-// and all of it is exact in c.  (c from some of the item's keys left dQ off by up
-// to 1.1e-2 where rows sit on other keys, 2.4e-3 now.)  (Delta from the stored O would carry
-// O's rounding to bf16, which the keys' common part lifts above the gradient
-// where many keys share a row: dQ was up to 7.2e-3 off.)
+//   dQ = scale (sum_j P (dP - c) K + f sum_j P K),    f = c - Delta,
+//   Delta = c + sum_j P (dP - c),
+// as sum_j P = 1 (but for the rounding of lse, which only scales f).  c is dO . O
+// with O as the forward stored it, rounded to bf16 on top, which is near Delta in
+// every row, so that f, and with it the rounding of P, is small.  (Delta from the
+// stored O would carry O's rounding to bf16, which the keys' common part lifts
+// above the gradient where many keys share a row.)
+// The sum over j of dS is zero, so what the keys have in common leaves dQ, but
+// roundings do not add up to zero: f is the sum of the rounded P (dP - c), negated,
+// so that the weights of K do.  dQ is off by 2.3e-3 of its norm then, as dK is, and
+// by 2.8e-3 where keys and values lie around 16 (2.8e-2 with f = c - Delta).  dS as
+// two bf16 and three products a step: 1.7e-3, but 360 us for both passes at 256x256
+// pixels, 346 so.
 // A query that sees one key alone has dS = 0: P is 1 whatever the score.
 //
 // S and dP have kStages stages in tensor memory, each with a group of four
@@ -90,7 +95,7 @@ template <int kSums, int kStages>
 struct RowSums {
   static constexpr int kHeld = kSums;
   bf16 c[2][128];
-  float2 sums[kSums][kStages][128];  // each group's sum P, sum P (dP - c)
+  float2 sums[kSums][kStages][128];  // each group's sum P (dP - c), and of the rounded terms
 };
 
 // Second pass: one more step of 16 along the heads' dimension adds -lse /
@@ -598,19 +603,19 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         mbar_arrive(rc.at(c_read));
         rc.next();
         if (!wait(rx.at(x_full), rx.parity)) break;
-        float sp = 0.f, sd = 0.f;
+        float sd = 0.f, sr = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const float2 x = S.side.sums[rx.i][g][r];
-          sp += x.x;
-          sd += x.y;
+          sd += x.x;
+          sr += x.y;
         }
         mbar_arrive(rx.at(x_read));
         rx.next();
-        const float delta = fmaf(c0, sp, sd), f = c0 - delta;
+        const float f = -sr;
         if (valid) {
-          if (p.nks > 1) p.part_s[it.split * rows + grow] = make_float4(c0, sp, sd, 1.f);
-          else p.delta[grow] = delta;
+          if (p.nks > 1) p.part_s[it.split * rows + grow] = make_float4(c0, sd, sr, 1.f);
+          else p.delta[grow] = c0 + sd;
         }
         if (!wait(acc_full, par)) break;
         tc_fence_after();
@@ -732,7 +737,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         const float nl = it.r0 + r < p.N ? neg_lse2(lse) : -INFINITY;  // rows past the end: probability zero
         const uint64_t nl2 = f2_make(nl, nl);
         bool have_c = false;
-        uint64_t c2 = 0, ls = 0, ds = 0;
+        uint64_t c2 = 0, ds = 0, rs = 0;
         const bool c_seen = look(rc.at(c_full), rc.parity);
         auto take_c = [&]() {
           have_c = true;
@@ -775,11 +780,11 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
               const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
               const uint64_t pp = f2_make(p0, p1);
               const uint64_t t = f2_mul(pp, f2_sub(f2_make(d[2 * i], d[2 * i + 1]), c2));
-              ls = f2_add(ls, pp);
               ds = f2_add(ds, t);
               const float2 tt = f2_split(t);
               pk[i] = pack_bf16(p0, p1);
               dk[i] = pack_bf16(tt.x, tt.y);
+              rs = f2_add(rs, f2_make(bf16x2_lo(dk[i]), bf16x2_hi(dk[i])));
             }
             tmem_st8u(ts + 8 * c, pk);
             tmem_st8u(ts + 64 + 8 * c, dk);
@@ -792,8 +797,8 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         if (!ok || (!have_c && !take_c())) break;
         j -= it.n;
         if (!wait(rx.at(x_read), rx.parity ^ 1u)) break;
-        const float2 l2 = f2_split(ls), d2 = f2_split(ds);
-        S.side.sums[rx.i][g][r] = make_float2(l2.x + l2.y, d2.x + d2.y);
+        const float2 d2 = f2_split(ds), r2 = f2_split(rs);
+        S.side.sums[rx.i][g][r] = make_float2(d2.x + d2.y, r2.x + r2.y);
         mbar_arrive(rx.at(x_full));
         rx.next();
       } else {
@@ -845,18 +850,18 @@ cross_dq_join(CrossParams p) {
   const size_t row = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
-  float delta = 0.f;
+  float c0 = 0.f, sd = 0.f, f = 0.f;
   for (int z = 0; z < p.nks; ++z) {
     const float4 s = p.part_s[z * rows + row];
-    delta += fmaf(s.x, s.y, s.z);
+    if (s.w != 0.f) c0 = s.x;  // the row's, in every split that has keys
+    sd += s.y;
+    f -= s.z;
   }
   float acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
   for (int z = 0; z < p.nks; ++z) {
-    const float4 s = p.part_s[z * rows + row];
-    if (s.w == 0.f) continue;  // a split without keys: its parts are not written
-    const float f = s.x - delta;
+    if (p.part_s[z * rows + row].w == 0.f) continue;  // a split without keys: its parts are not written
     const size_t at = (z * rows + row) * D + lane * C;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] += fmaf(f, p.part_dqb[at + c], p.part_dq[at + c]);
@@ -865,7 +870,7 @@ cross_dq_join(CrossParams p) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
     store_elem(static_cast<bf16*>(p.dq) + row * D + lane * C + c, one ? 0.f : acc[c] * p.scale);
-  if (lane == 0) p.delta[row] = delta;
+  if (lane == 0) p.delta[row] = c0 + sd;
 }
 
 // The second pass's shares of a key tile summed: D / 4 threads per key and

@@ -11,11 +11,14 @@ that are spread evenly by logarithm, sqrt(3/4 / (2 ln 2)).  With P and dS rounde
 for the products and the result rounded once,
     |err dV|^2 = R^2 (sum_ij P_ij^2 |dO_i|^2            + |dV|^2)
     |err dK|^2 = R^2 (scale^2 sum_ij dS_ij^2 |q_i|^2    + |dK|^2)
-    |err dQ|^2 = R^2 (scale^2 sum_ij dS_ij^2 |k_j|^2    + |dQ|^2)
-where the first pass rounds P (dP - c) and P in place of dS, with c within a few
-bf16 roundings of Delta, which changes neither sum by more than their square.  All
-three are held to 1.5 of the total, as thousands of roundings add up to their mean
-square.
+    |err dQ|^2 = R^2 (scale^2 sum_ij (dS_ij^2 + P_ij^2 f_i^2) |k_j - m_i|^2 + |dQ|^2)
+as the first pass rounds P (dP - c), and P for its product with f = c - Delta, and
+f makes the rounded weights of the keys add up to zero, so that any m_i may be
+taken off them: the mean by P, of a row.  c = dO . O carries O's rounding, those
+of the sums of up to four products that a lane keeps in bf16 (1 + 2 + 3 + 4 squares
+of products for four) and its own: f_i^2 = R^2 (3.5 sum_d (dO_d O_d)^2 + Delta_i^2).
+All three are held to 1.5 of the total, as thousands of roundings add up to their
+mean square.
 
 fp32: a sum of n products is off by sqrt(n) u of its terms' absolute sum, u =
 2^-24 (roundings of independent signs), which carries through the formula
@@ -58,7 +61,10 @@ def expected(x, want, kv_len, mask):
     ds = p * (dp - delta)
     if x["q"].dtype == torch.bfloat16:
         sq = (lambda t: (t * t).sum(-1))
-        sums = {"dq": scale**2 * ((ds * ds) @ sq(k)[..., None]).sum(),
+        f2 = R**2 * (3.5 * sq(do * (p @ v)) + sq(delta))[..., None]
+        w, m = ds * ds + p * p * f2, p @ k  # sum_j w |k - m|^2, written out
+        spread = w @ sq(k)[..., None] - 2 * (m * (w @ k)).sum(-1, keepdim=True) + w.sum(-1, keepdim=True) * sq(m)[..., None]
+        sums = {"dq": scale**2 * spread.clamp_min(0.0).sum(),
                 "dk": scale**2 * ((ds * ds).mT @ sq(q)[..., None]).sum(),
                 "dv": ((p * p).mT @ sq(do)[..., None]).sum()}
         return {n: 1.5 * R * float(t + sq(want[n][0]).sum()) ** 0.5 for n, t in sums.items()}
