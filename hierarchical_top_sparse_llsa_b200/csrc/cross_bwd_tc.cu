@@ -37,7 +37,7 @@
 //   load    TMA loads of A (two buffers) and N (a ring);
 //   mma     issues S and dP; prod the products.  One warp for both would leave
 //           the tensor cores idle between its waits;
-//   dot     (four) first pass: c;
+//   dot     (four or eight) first pass: c;
 //   aux     first pass: with lengths or a mask, the bits of the keys seen and
 //           zeros over the K rows that are not (their dS is zero, and zero
 //           times NaN is NaN); second pass: lse and Delta of the queries that
@@ -72,7 +72,10 @@ struct Sizes {
   // warp sees every round of its slots: a barrier is not waited for before the
   // round before has been seen, which its parity would not tell apart.
   static constexpr int kAuxWarps = 3;
-  static constexpr int kDot = kAux + kAuxWarps;  // first pass: four warps for c
+  // First pass: sets of four warps for c, which take turns.  Two where registers
+  // allow: D = 128 against 80 keys 196 us, 208 with one.
+  static constexpr int kDot = kAux + kAuxWarps;
+  static constexpr int kDotSets = (D == 64) ? 1 : 2;
   static constexpr int kA = 128 * D * 2;   // a tile of A1 or A2
   static constexpr int kN = 64 * D * 2;    // a tile of N1 or N2
   static constexpr int kSlots = (D == 64) ? 6 : 3;
@@ -113,7 +116,7 @@ struct ColumnTerms {
 template <int D, bool kDq>
 struct Cfg : Sizes<D> {
   using Z = Sizes<D>;
-  static constexpr int kThreads = (Z::kDot + (kDq ? 4 : 0)) * 32;
+  static constexpr int kThreads = (Z::kDot + (kDq ? 4 * Z::kDotSets : 0)) * 32;
   // buffers of A1, A2: the second pass has few items
   static constexpr int kBufs = (D == 64 || kDq) ? 2 : 1;
   static constexpr int kOffN = kBufs * 2 * Z::kA;
@@ -445,13 +448,18 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
     // such steps, whose sums over the lanes then end in one lane each.  A lane
     // adds its eight products in bf16: any c is right, and this one as near.  dO
     // is read again rather than taken from its tile, so that c does not wait for
-    // that (336 us against 340 at 256x256 pixels, D = 128 182 against 188).
+    // that (336 us against 340 at 256x256 pixels, D = 128 182 against 188).  Reading
+    // O is what the pass takes longer for where it is bound by memory.
     if constexpr (kDq) {
       constexpr int L = D / 8, kRows = 32 / L;
-      const int first = 32 * (warp - C::kDot) + lane / L, chunk = lane % L;
+      const int first = 32 * ((warp - C::kDot) & 3) + lane / L, chunk = lane % L;
       Ring<2> rc;
+      int turn = (warp - C::kDot) >> 2;  // items of the other set before this one's next
+      rc.next(turn);
       for (; ok && it.next();) {
         if (it.n == 0) continue;
+        if (C::kDotSets > 1 && turn-- > 0) continue;
+        turn = C::kDotSets - 1;
         const size_t at = ((size_t)it.bk * p.N + it.r0 + first) * L + chunk;
         const uint4 *o = static_cast<const uint4*>(p.o_in) + at, *g = static_cast<const uint4*>(p.dout) + at;
         float s[L];
@@ -487,7 +495,7 @@ cross_bwd_tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_consta
         if (!wait(rc.at(c_read), rc.parity ^ 1u)) break;
         S.side.c[rc.i][first + chunk * kRows] = __float2bfloat16_rn(fabsf(s[0]) < 3e38f ? s[0] : 0.f);
         mbar_arrive(rc.at(c_full));
-        rc.next();
+        rc.next(C::kDotSets);
       }
     }
   } else if (warp >= C::kAux) {
