@@ -4,12 +4,13 @@
 //   s = scale q k^T, P = e^(s - lse), O = P V / l
 //   dV = P^T dO, dS = P (dO V^T - Delta), dQ = scale dS K, dK = scale dS^T Q
 //
-// Tensor-core formats hold too few bits for fp32 inputs.  19 to 22 TFLOP/s at
-// 16384 queries x 256 keys, of about 74: by count the FMAs wait for the loads
-// from shared memory (16 bytes a thread take 9 cycles an SM).  A thread holds a block of the tile in registers (8 x 4 scores in
-// the forward) and feeds it with 16-byte shared-memory loads, rows padded so
-// that the 16 keys a half warp reads sit in different banks.  Probabilities
-// pass through shared memory, over the K tile that is no longer read.
+// Tensor-core formats hold too few bits for fp32 inputs.  A thread holds a block
+// of the tile in registers (8 x 4 scores in the forward) and feeds it with 16-byte
+// shared-memory loads, rows padded so that the 16 keys a half warp reads sit in
+// different banks.  Probabilities pass through shared memory, over the K tile that
+// is no longer read.  19 to 22 TFLOP/s at 16384 queries x 256 keys, of about 74: by
+// count the FMAs wait for the loads from shared memory (16 bytes a thread take 9
+// cycles an SM).
 // The forward is cut along the keys, dQ likewise, and dK with dV along the
 // query tiles, where whole tiles would leave SMs idle; the parts are fp32 and
 // joined in a fixed order.  A key that is not seen is stored as zeros and its

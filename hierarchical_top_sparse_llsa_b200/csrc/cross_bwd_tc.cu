@@ -45,10 +45,11 @@
 // The second pass cuts all its (key tile, query tile) pairs into equal runs,
 // one per SM; a key tile that several SMs share is summed by a last kernel, in
 // a fixed order.  The first pass cuts the keys where there are few rows.
-// 32768 queries x 16 heads x 256 keys, D = 64: 106 us and 83 us, the tensor
-// cores busy for 34% and 51%, the special-function units for 37% and 46%.  With
-// row work, MMAs and loads left out 63% and 47% of the cycles remained: the
-// chain of waits (scores, row work, products, scores) is the largest part.
+// 32768 queries x 16 heads x 256 keys, D = 64: 106 us and 82 us, the tensor
+// cores busy for 33% and 51%, the special-function units for 35% and 45%.  With
+// row work, MMAs and loads left out 63% and 47% of the cycles remained (before O
+// was read): the chain of waits (scores, row work, products, scores) is the
+// largest part.
 // Every wait is bounded; a time-out is reported as LLSA_DEV_TIMEOUT.
 
 #include <math.h>

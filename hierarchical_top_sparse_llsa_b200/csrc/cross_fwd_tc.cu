@@ -21,9 +21,9 @@
 //   store  TMA stores of the finished O tiles, staged over their Q.
 // The query tiles take turns: the tensor cores work on some while the
 // exponentials of the others are computed (one per score; 16 a clock and SM).
-// 65536 queries x 16 heads x 256 keys of D = 64 take 127 to 138 us (42 us of
-// memory, 60 of exponentials): the special-function units are busy for 51% of
-// the time, the tensor cores for 25%, the rest is waits between the warps.
+// 65536 queries x 16 heads x 256 keys of D = 64 take 136 to 139 us (42 us of
+// memory, 60 of exponentials): the special-function units are busy for 50% of
+// the time, the tensor cores for 24%, the rest is waits between the warps.
 // At D = 64 four query tiles are in flight, each
 // against 64 keys at a time; at D = 128 tensor memory holds two, and they take
 // 128 keys, an N that the tensor cores run at full rate (two tiles of 128 keys at

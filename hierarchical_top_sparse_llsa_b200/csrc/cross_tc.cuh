@@ -1,4 +1,5 @@
-// What the tcgen05 cross-attention kernels share: the walk over work items.
+// What the tcgen05 cross-attention kernels share: tile addresses, barrier waits,
+// rings of slots, hidden keys.
 #pragma once
 
 #include "cross.cuh"

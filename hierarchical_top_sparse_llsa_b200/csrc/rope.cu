@@ -255,7 +255,8 @@ rope_kernel(RopeParams p) {
 }
 
 // The half layout where a partner sits off the 16-byte chunks: a thread per
-// pair (or per two channels that pass through), element by element.
+// pair (or per two channels that pass through), element by element.  Q and K of
+// 24 heads, 16384 tokens of bf16, with 12 or 30 pairs 141 and 131 us, 45 in chunks.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_ragged_kernel(RopeParams p) {
